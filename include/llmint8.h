@@ -26,7 +26,8 @@
  *     out) are written to the status word of the workspace; read them with
  *     llmint8_device_status().  Each call that takes a workspace overwrites that word.
  *   - Shapes: M >= 1; K and N are multiples of 16 and >= 16; K <= 131072 (so that
- *     |C| <= K * 127^2 < 2^31).  Violations return LLMINT8_ERR_UNSUPPORTED_SHAPE.
+ *     |C| <= K * 127^2 < 2^31).  Violations return LLMINT8_ERR_UNSUPPORTED_SHAPE.  (The MXFP4
+ *     calls and the residual norm at the end of this file state their own shapes.)
  *   - No C++ exception crosses this interface.
  */
 #ifndef LLMINT8_H
@@ -336,6 +337,125 @@ LLMINT8_API llmint8_status llmint8_linear_noalloc(const uint16_t *X, int64_t M, 
                                       const uint16_t *bias, const uint16_t *W_fp16,
                                       float threshold, int64_t max_outliers, uint16_t *Y,
                                       void *stream, void **scratch_out);
+
+/*
+ * MXFP4: 4-bit floating point with one power-of-two scale to 32 elements (the OCP microscaling
+ * format MXFP4), quantisation and product.  The pages stop at 8 bits; these calls stand beside
+ * the int8 ones for weights and activations of half that size, which sm_100a's tensor cores
+ * multiply natively.
+ *
+ * An MXFP4 matrix of R rows and K columns is
+ *   codes   uint8 [R, K/2], row-major: element k of a row in the low (k even) or high (k odd) four
+ *           bits of byte k / 2.  A code is an e2m1 float: sign (8), then 0, .5, 1, 1.5, 2, 3, 4, 6.
+ *   scales  uint8 [ceil(R/128)][ceil(K/256)][1024]: one e8m0 byte s, the scale 2^(s - 127) (255
+ *           means NaN), to 32 consecutive elements of a row, in tiles of 128 rows x 256 columns:
+ *           block b (of 8) of the tile's row r lies at byte 512 (b / 4) + 16 (r % 32) +
+ *           4 (r / 32) + b % 4.  Bytes of rows >= R and columns >= K are padding; they may hold
+ *           anything but 255 (the calls here write 0).
+ * Both are 16-byte aligned.  R >= 0, K a multiple of 32, 32 <= K <= 131072; a matrix of no rows is
+ * valid, and a call on it succeeds without a launch (its pointers may then be NULL).
+ *
+ * Quantisation of a block x[0..32): the scale is 2^(floor(log2 max|x|) - 2), not below 2^-127
+ * (a block of zeros takes that one); the codes are x / scale rounded to nearest, ties to the even
+ * code, values beyond 6 to 6.  A block holding a NaN or an infinity gets the NaN scale: all its
+ * elements then read as NaN.
+ */
+typedef enum {
+    LLMINT8_F16 = 0,  /* IEEE binary16 */
+    LLMINT8_BF16 = 1, /* bfloat16 */
+    LLMINT8_F32 = 2   /* IEEE binary32 */
+} llmint8_dtype;
+
+/* Bytes of the scales of an R x K matrix; 0 for shapes outside the rules (and for R = 0). */
+LLMINT8_API size_t llmint8_mxfp4_scales_size(int64_t R, int64_t K);
+
+/*
+ * Rows of a matrix (a weight [N, K], or activations [M, K]) to MXFP4.
+ *   X       [R, K] of `dtype` (any llmint8_dtype), rows ldx elements apart: ldx >= K and a row
+ *           pitch that is a multiple of 16 bytes (else LLMINT8_ERR_INVALID_ARG).
+ *   codes, scales  outputs, padding included.
+ * Pure function of X: calling it twice gives identical bytes.
+ */
+LLMINT8_API llmint8_status llmint8_mxfp4_quantize(const void *X, int dtype, int64_t R, int64_t K,
+                                      int64_t ldx, uint8_t *codes, uint8_t *scales,
+                                      void *stream);
+
+/* MXFP4 to values: out [R, K] of `dtype` (any llmint8_dtype), code * scale rounded once. */
+LLMINT8_API llmint8_status llmint8_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales,
+                                     int64_t R, int64_t K, void *out, int dtype, void *stream);
+
+/*
+ * The MXFP4 linear layer Y = q(X) . W^T + bias: X is quantised to MXFP4 in the call and multiplied
+ * with the MXFP4 weight on the tensor cores; products of codes are exact, sums are fp32, and Y is
+ * rounded once.
+ *   X       [M, K] of `dtype` (LLMINT8_F16 or LLMINT8_BF16), rows ldx elements apart (rules as in
+ *           llmint8_mxfp4_quantize).
+ *   Wc, Ws  MXFP4 weight [N, K], N >= 1 (any N).
+ *   bias    [N] of `dtype`, or NULL.
+ *   Y       [M, N] of `dtype`, dense.
+ *   ws      device workspace of llmint8_mxfp4_linear_workspace_size(M, N, K) bytes; its device
+ *           status is read with llmint8_device_status().  Calls that may overlap need a workspace
+ *           each; calls in stream order may share one.
+ * Kernels: at most 256 rows of X stream the weight as the MMA's 128-row operand, k split over the
+ * CTAs of a cluster; more run CTA pairs on 256 x 256 tiles.  Results do not depend on timing; the
+ * same rows in calls of different M may differ in the last fp32 rounding of a sum.
+ */
+LLMINT8_API llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t K,
+                                    int64_t ldx, const uint8_t *Wc, const uint8_t *Ws, int64_t N,
+                                    const void *bias, void *Y, void *ws, size_t ws_bytes,
+                                    void *stream);
+
+LLMINT8_API size_t llmint8_mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+
+/*
+ * llmint8_mxfp4_linear with X already MXFP4 (from llmint8_mxfp4_quantize or
+ * llmint8_residual_norm): the same Y, bit for bit, without the quantisation's launch.  ws: 256
+ * bytes (the status header).
+ */
+LLMINT8_API llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, const uint8_t *Xs,
+                                              int64_t M, int64_t K, const uint8_t *Wc,
+                                              const uint8_t *Ws, int64_t N, const void *bias,
+                                              void *Y, int dtype, void *ws, size_t ws_bytes,
+                                              void *stream);
+
+/*
+ * The step between two blocks of a transformer, which produces a layer's input:
+ *     h = residual + scale * gate * PostNorm(x)
+ *     y = Norm(h)
+ * A norm of a row v is v / sqrt(mean(v^2) + eps) * weight + bias (LLMINT8_NORM_RMS) or the same
+ * of v - mean(v) (LLMINT8_NORM_LAYER).  y leaves as 16-bit values, as the MXFP4 operand of
+ * llmint8_mxfp4_linear_quantized, or both.  Arithmetic is fp32; h and y are each rounded once (y
+ * from the unrounded h), and the MXFP4 form is llmint8_mxfp4_quantize's of the rounded y.
+ *   X          [M, K] of `dtype` (LLMINT8_F16 or LLMINT8_BF16), rows ldx elements apart (rules as
+ *              in llmint8_mxfp4_quantize).
+ *   residual   [M, K], rows ldr elements apart, or NULL (taken as 0).
+ *   post_norm  a llmint8_norm; LLMINT8_NORM_NONE takes x as it is.  post_weight, post_bias: [K]
+ *              or NULL (1 and 0).
+ *   gate       [gate_rows, K] or NULL (1): row m takes gate row m / (M / gate_rows), so gate_rows
+ *              = 1 is one gate for all rows, = M one each, and a batch of sequences of equal
+ *              length has one each.  gate_rows must divide M.
+ *   norm       LLMINT8_NORM_NONE leaves y out (Y, codes and scales must then be NULL).  weight,
+ *              bias: [K] or NULL.
+ *   eps        >= 0, for both norms.
+ *   H          [M, K] output, or NULL.  May be the residual's or X's own (dense) buffer.
+ *   Y          [M, K] output, or NULL.  May be X's own buffer.
+ *   codes, scales  MXFP4 form of y (both or neither NULL), padding included.
+ * At least one output is given.  K <= 32768 here (a row lives in one CTA's registers); every
+ * pointer is 16-byte aligned; all vectors are of `dtype`.
+ */
+typedef enum {
+    LLMINT8_NORM_NONE = 0,
+    LLMINT8_NORM_RMS = 1,
+    LLMINT8_NORM_LAYER = 2
+} llmint8_norm;
+
+LLMINT8_API llmint8_status llmint8_residual_norm(const void *X, int dtype, int64_t M, int64_t K,
+                                     int64_t ldx, const void *residual, int64_t ldr,
+                                     int post_norm, const void *post_weight,
+                                     const void *post_bias, const void *gate, int64_t gate_rows,
+                                     float scale, int norm, const void *weight, const void *bias,
+                                     float eps, void *H, void *Y, uint8_t *codes,
+                                     uint8_t *scales, void *stream);
 
 #ifdef __cplusplus
 }

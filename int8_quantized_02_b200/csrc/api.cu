@@ -653,3 +653,201 @@ llmint8_status llmint8_linear_noalloc(const uint16_t *X, int64_t M, int64_t K, c
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------- MXFP4 and the residual norm ---
+
+namespace {
+
+bool mx_k_ok(int64_t K) { return K >= 32 && K % 32 == 0 && K <= 131072; }
+bool mx_rows_ok(int64_t R) { return R >= 0 && R <= (int64_t)INT32_MAX; }
+bool dtype16(int dtype) { return dtype == LLMINT8_F16 || dtype == LLMINT8_BF16; }
+// A row pitch of `ld` elements of `bytes` bytes: at least K, each row on 16 bytes.
+bool pitch_ok(int64_t ld, int64_t K, int bytes) {
+    return ld >= K && ld <= INT64_MAX / 16 && ld * bytes % 16 == 0;
+}
+bool mx_pair_ok(const uint8_t *codes, const uint8_t *scales) {
+    return codes && scales && aligned16(codes) && aligned16(scales);
+}
+
+size_t mx_scales_bytes(int64_t R, int64_t K) {
+    return (size_t)(ceil_div(R, 128) * ceil_div(K, 256) * 1024);
+}
+
+// Workspace of llmint8_mxfp4_linear: the status header, X's codes and scales.
+struct Mxfp4Layout {
+    size_t codes = 0, scales = 0, total = 0;
+};
+Mxfp4Layout mxfp4_layout(int64_t M, int64_t K) {
+    Mxfp4Layout L;
+    L.codes = sizeof(WsHeader);
+    L.scales = (size_t)align_up((int64_t)L.codes + M * (K / 2), 256);
+    L.total = L.scales + mx_scales_bytes(M, K);
+    return L;
+}
+
+// The checks that the two linear calls share, X apart.
+llmint8_status check_mxfp4(int dtype, int64_t M, int64_t K, const uint8_t *Wc, const uint8_t *Ws,
+                           int64_t N, const void *bias, const void *Y, const void *ws,
+                           size_t ws_bytes, size_t need) {
+    if (!dtype16(dtype)) return LLMINT8_ERR_INVALID_ARG;
+    if (!mx_rows_ok(M) || !mx_k_ok(K) || N < 1 || N > (int64_t)INT32_MAX)
+        return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return LLMINT8_OK;
+    if (!mx_pair_ok(Wc, Ws) || !Y || !ws || !aligned16(Y) || !aligned16(ws) ||
+        (bias && !aligned16(bias)))
+        return LLMINT8_ERR_INVALID_ARG;
+    return ws_bytes < need ? LLMINT8_ERR_WORKSPACE_TOO_SMALL : LLMINT8_OK;
+}
+
+// The product between the process-wide profile events (when set).
+llmint8_status run_mxfp4(const uint8_t *Xc, const uint8_t *Xs, int64_t M, int64_t K,
+                         const uint8_t *Wc, const uint8_t *Ws, int64_t N, const void *bias,
+                         void *Y, int dtype, int weights_ready, void *ws, cudaStream_t s) {
+    Mxfp4Gemm g;
+    g.Xc = Xc;
+    g.Xs = Xs;
+    g.Wc = Wc;
+    g.Ws = Ws;
+    g.bias = bias;
+    g.Y = Y;
+    g.dtype = dtype;
+    g.weights_ready = weights_ready;
+    g.status = next_status(at<WsHeader>(ws, 0));
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.timeout_ns = g_timeout_ns.load();
+    cudaEvent_t ev0 = g_prof_start.load(), ev1 = g_prof_stop.load();
+    if (ev0) {
+        // the event's record stands between the quantisation and the product
+        g.weights_ready = 0;
+        if (record_profile_event(ev0, s) != cudaSuccess) return LLMINT8_ERR_CUDA;
+    }
+    if (launch_mxfp4_gemm(g, s) != cudaSuccess) return LLMINT8_ERR_CUDA;
+    if (ev1 && record_profile_event(ev1, s) != cudaSuccess) return LLMINT8_ERR_CUDA;
+    return LLMINT8_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t llmint8_mxfp4_scales_size(int64_t R, int64_t K) {
+    return mx_rows_ok(R) && mx_k_ok(K) ? mx_scales_bytes(R, K) : 0;
+}
+
+size_t llmint8_mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
+    if (!mx_rows_ok(M) || !mx_k_ok(K) || N < 1 || N > (int64_t)INT32_MAX) return 0;
+    return mxfp4_layout(M, K).total;
+}
+
+llmint8_status llmint8_mxfp4_quantize(const void *X, int dtype, int64_t R, int64_t K, int64_t ldx,
+                                      uint8_t *codes, uint8_t *scales, void *stream) {
+    LLMINT8_CALL_RANGE();
+    if (!dtype16(dtype) && dtype != LLMINT8_F32) return LLMINT8_ERR_INVALID_ARG;
+    if (!mx_rows_ok(R) || !mx_k_ok(K)) return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    if (R == 0) return LLMINT8_OK;
+    if (!X || !aligned16(X) || !mx_pair_ok(codes, scales) ||
+        !pitch_ok(ldx, K, dtype == LLMINT8_F32 ? 4 : 2))
+        return LLMINT8_ERR_INVALID_ARG;
+    return from_cuda(launch_mxfp4_quantize(X, dtype, ldx, R, align_up(R, 128), K, codes, scales,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+llmint8_status llmint8_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t R,
+                                     int64_t K, void *out, int dtype, void *stream) {
+    LLMINT8_CALL_RANGE();
+    if (!dtype16(dtype) && dtype != LLMINT8_F32) return LLMINT8_ERR_INVALID_ARG;
+    if (!mx_rows_ok(R) || !mx_k_ok(K)) return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    if (R == 0) return LLMINT8_OK;
+    if (!mx_pair_ok(codes, scales) || !out || !aligned16(out)) return LLMINT8_ERR_INVALID_ARG;
+    return from_cuda(launch_mxfp4_dequant(codes, scales, R, K, out, dtype,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t K, int64_t ldx,
+                                    const uint8_t *Wc, const uint8_t *Ws, int64_t N,
+                                    const void *bias, void *Y, void *ws, size_t ws_bytes,
+                                    void *stream) {
+    LLMINT8_CALL_RANGE();
+    const size_t need = llmint8_mxfp4_linear_workspace_size(M, N, K);
+    const llmint8_status chk =
+        check_mxfp4(dtype, M, K, Wc, Ws, N, bias, Y, ws, ws_bytes, need);
+    if (chk != LLMINT8_OK) return chk;
+    if (M == 0) return LLMINT8_OK;
+    if (!X || !aligned16(X) || !pitch_ok(ldx, K, 2)) return LLMINT8_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Mxfp4Layout L = mxfp4_layout(M, K);
+    uint8_t *Xc = at<uint8_t>(ws, L.codes), *Xs = at<uint8_t>(ws, L.scales);
+    // rows past M of the last scale tile meet only codes that read as zero, in columns of the
+    // product that are not stored: they stay as they are
+    if (launch_mxfp4_quantize(X, dtype, ldx, M, M, K, Xc, Xs, s) != cudaSuccess)
+        return LLMINT8_ERR_CUDA;
+    return run_mxfp4(Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 1, ws, s);
+}
+
+llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, const uint8_t *Xs, int64_t M,
+                                              int64_t K, const uint8_t *Wc, const uint8_t *Ws,
+                                              int64_t N, const void *bias, void *Y, int dtype,
+                                              void *ws, size_t ws_bytes, void *stream) {
+    LLMINT8_CALL_RANGE();
+    const llmint8_status chk =
+        check_mxfp4(dtype, M, K, Wc, Ws, N, bias, Y, ws, ws_bytes, sizeof(WsHeader));
+    if (chk != LLMINT8_OK) return chk;
+    if (M == 0) return LLMINT8_OK;
+    if (!mx_pair_ok(Xc, Xs)) return LLMINT8_ERR_INVALID_ARG;
+    return run_mxfp4(Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 0, ws,
+                     static_cast<cudaStream_t>(stream));
+}
+
+llmint8_status llmint8_residual_norm(const void *X, int dtype, int64_t M, int64_t K, int64_t ldx,
+                                     const void *residual, int64_t ldr, int post_norm,
+                                     const void *post_weight, const void *post_bias,
+                                     const void *gate, int64_t gate_rows, float scale, int norm,
+                                     const void *weight, const void *bias, float eps, void *H,
+                                     void *Y, uint8_t *codes, uint8_t *scales, void *stream) {
+    LLMINT8_CALL_RANGE();
+    const auto norm_ok = [](int n) { return n >= LLMINT8_NORM_NONE && n <= LLMINT8_NORM_LAYER; };
+    if (!dtype16(dtype) || !norm_ok(norm) || !norm_ok(post_norm) || !(eps >= 0.0f) || isinf(eps))
+        return LLMINT8_ERR_INVALID_ARG;
+    if (!mx_rows_ok(M) || !mx_k_ok(K) || K > kNormMaxK) return LLMINT8_ERR_UNSUPPORTED_SHAPE;
+    if (M == 0) return LLMINT8_OK;
+    if (!X || !pitch_ok(ldx, K, 2) || (residual && !pitch_ok(ldr, K, 2)))
+        return LLMINT8_ERR_INVALID_ARG;
+    for (const void *p : {X, residual, post_weight, post_bias, gate, weight, bias,
+                          static_cast<const void *>(H), static_cast<const void *>(Y),
+                          static_cast<const void *>(codes), static_cast<const void *>(scales)})
+        if (p && !aligned16(p)) return LLMINT8_ERR_INVALID_ARG;
+    if ((codes == nullptr) != (scales == nullptr)) return LLMINT8_ERR_INVALID_ARG;
+    if (norm == LLMINT8_NORM_NONE && (Y || codes || weight || bias)) return LLMINT8_ERR_INVALID_ARG;
+    if (norm != LLMINT8_NORM_NONE && !Y && !codes) return LLMINT8_ERR_INVALID_ARG;
+    if (post_norm == LLMINT8_NORM_NONE && (post_weight || post_bias)) return LLMINT8_ERR_INVALID_ARG;
+    if (!H && !Y && !codes) return LLMINT8_ERR_INVALID_ARG;
+    if (gate && (gate_rows < 1 || M % gate_rows != 0)) return LLMINT8_ERR_INVALID_ARG;
+    NormArgs a;
+    a.X = X;
+    a.residual = residual;
+    a.post_weight = post_weight;
+    a.post_bias = post_bias;
+    a.gate = gate;
+    a.weight = weight;
+    a.bias = bias;
+    a.H = H;
+    a.Y = Y;
+    a.codes = codes;
+    a.scales = scales;
+    a.M = M;
+    a.K = K;
+    a.ldx = ldx;
+    a.ldr = ldr;
+    a.gate_group = gate ? M / gate_rows : 1;
+    a.rows_out = align_up(M, 128);
+    a.tiles_k = ceil_div(K, 256);
+    a.norm = norm;
+    a.post_norm = post_norm;
+    a.scale = scale;
+    a.eps = eps;
+    return from_cuda(launch_residual_norm(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

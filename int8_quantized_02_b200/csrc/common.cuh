@@ -36,6 +36,15 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
     return t;
 }
 
+// Programmatic dependent launch: every kernel of a layer call is launched so that its CTAs
+// may start while the previous kernel in the stream finishes.  Each waits for that kernel
+// (and so for everything before it) before it touches global memory, and lets the next one
+// launch right away.
+__device__ __forceinline__ void pdl_wait_then_release() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ------------------------------------------------------------------ mbarrier ----------
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
@@ -45,6 +54,12 @@ __device__ __forceinline__ void fence_mbar_init() {
 }
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+// Takes bytes off the current phase's pending count, as a copy that lands does.
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
@@ -344,6 +359,64 @@ __host__ __device__ __forceinline__ int rotated_kblock(int it, int tile, int kbl
     const int r = (int)(((unsigned)tile * 7u) % (unsigned)kblocks);
     const int kb = it + r;
     return kb >= kblocks ? kb - kblocks : kb;
+}
+
+// ---- CTA-pair forms (tcgen05 cta_group::2).  The pair's leader (rank 0) issues the MMAs;
+// operand addresses are the same shared-memory offsets in both CTAs.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *tm, int x,
+                                                 int y, uint32_t bar_cluster) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar_cluster)
+        : "memory");
+}
+// The same loads with an L2 eviction policy.  The quantized rows of X are re-read by every wave
+// of output tiles (the tiles walk M fastest), so their loads ask L2 to evict them last; the
+// weight loads keep the default policy (the 16 M tiles of a weight tile do not all run at the
+// same moment, and evict-first weights were re-read from HBM: 2.78 against 1.72 GB per
+// launch on the int8 175B projection, while evict-last Xq alone gives 1.55 GB).
+__device__ __forceinline__ uint64_t l2_policy_evict_last() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap *tm, int x, int y,
+                                                 uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(pol)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair_hint(uint32_t dst, const CUtensorMap *tm, int x,
+                                                      int y, uint32_t bar_cluster, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar_cluster), "l"(pol)
+        : "memory");
+}
+// Arrive on the barrier at `bar` in both CTAs of the pair once the pair's MMAs issued so far
+// by this thread have completed: one commit for each CTA's barrier (a commit tracks every
+// earlier tcgen05 operation of the thread, so the two arrive at the same point).
+__device__ __forceinline__ void tc_commit_pair_both(uint32_t bar) {
+#pragma unroll
+    for (uint32_t r = 0; r < 2; ++r)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                map_to_rank(bar, r))
+            : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
+                 "r"(ncols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                 : "memory");
 }
 
 // Instruction descriptors (kind::i8 and kind::f16), K-major A and B, dense.

@@ -38,6 +38,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 
 namespace llmint8 {
 
@@ -865,19 +866,6 @@ llmint8_decode_kernel(const __grid_constant__ CUtensorMap tmCB, const DArgs a) {
     }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
 }  // namespace
 
 DecodePlan decode_plan(int64_t M, int64_t N, int64_t K, int64_t cap, int sms) {
@@ -982,7 +970,7 @@ cudaError_t launch_decode(const DecodeLaunch &d, cudaStream_t s) {
     a.ring_off = p.ring_off;
     a.timeout_ns = d.timeout_ns;
 
-    auto enc = encoder();
+    auto enc = tensor_map_encoder();
     if (!enc) return cudaErrorInvalidValue;
     CUtensorMap tm;
     cuuint64_t dims[2] = {(cuuint64_t)d.K, (cuuint64_t)d.N};

@@ -35,12 +35,11 @@
 // copies and MMAs in flight, frees TMEM and returns.  A pair's CTAs exit only after the
 // leader has drained the loads of both and the second CTA has made its last arrive on the
 // leader's barriers.
-#include <cudaTypedefs.h>
-
 #include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 
 namespace llmint8 {
 
@@ -118,42 +117,7 @@ struct Args {
     uint64_t timeout_ns;
 };
 
-// ---- CTA-pair forms (tcgen05 cta_group::2).  The pair's leader (rank 0) issues the MMAs;
-// operand addresses are the same shared-memory offsets in both CTAs.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *tm, int x,
-                                                 int y, uint32_t bar_cluster) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar_cluster)
-        : "memory");
-}
-// The same loads with an L2 eviction policy.  The quantized rows Xq are re-read by every wave
-// of output tiles (the tiles walk M fastest), so their loads ask L2 to evict them last; the
-// weight loads keep the default policy (the 16 M tiles of a weight tile do not all run at the
-// same moment, and evict-first weights were re-read from HBM: 2.78 against 1.72 GB per
-// launch on the 175B projection, while evict-last Xq alone gives 1.55 GB).
-__device__ __forceinline__ uint64_t l2_policy_evict_last() {
-    uint64_t p;
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
-    return p;
-}
-__device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap *tm, int x, int y,
-                                                 uint32_t bar, uint64_t pol) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar), "l"(pol)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_pair_hint(uint32_t dst, const CUtensorMap *tm, int x,
-                                                      int y, uint32_t bar_cluster, uint64_t pol) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        ".L2::cache_hint [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tm)), "r"(x), "r"(y), "r"(bar_cluster), "l"(pol)
-        : "memory");
-}
+// ---- CTA-pair MMAs (cta_group::2), issued by the pair's leader.
 __device__ __forceinline__ void mma_i8_pair(uint32_t d, uint64_t adesc, uint64_t bdesc,
                                             uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -172,28 +136,6 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t adesc, uint64_
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// Arrive on the barrier at `bar` in both CTAs of the pair once the pair's MMAs issued so far
-// by this thread have completed: one commit for each CTA's barrier (a commit tracks every
-// earlier tcgen05 operation of the thread, so the two arrive at the same point).
-__device__ __forceinline__ void tc_commit_pair_both(uint32_t bar) {
-#pragma unroll
-    for (uint32_t r = 0; r < 2; ++r)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                map_to_rank(bar, r))
-            : "memory");
-}
-__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
-
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
     __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&h);
@@ -624,35 +566,6 @@ LLMINT8_GEMM_KERNEL(llmint8_gemm_pair_kernel, true, false)
 LLMINT8_GEMM_KERNEL(llmint8_gemm_bits_kernel, false, true)
 LLMINT8_GEMM_KERNEL(llmint8_gemm_pair_bits_kernel, true, true)
 #undef LLMINT8_GEMM_KERNEL
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    return fn;
-}
-
-// 2-D row-major map over [rows, cols] elements with a (box_cols x box_rows) box, 128 B swizzle.
-bool make_map(CUtensorMap *tm, const void *base, CUtensorMapDataType dt, int elem_bytes,
-              int64_t cols, int64_t rows, int64_t pitch_elems, uint32_t box_cols,
-              uint32_t box_rows) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)(pitch_elems * elem_bytes)};
-    cuuint32_t box[2] = {box_cols, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return enc(tm, dt, 2, const_cast<void *>(base), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 struct DeviceInfo {
     int sms = 0;

@@ -145,3 +145,47 @@ struct DecodeLaunch {
 cudaError_t launch_decode(const DecodeLaunch &d, cudaStream_t s);
 
 }  // namespace llmint8
+
+namespace llmint8 {
+
+// MXFP4 (mxfp4.cu): codes uint8 [R, K/2], scales uint8 [ceil(R/128)][ceil(K/256)][1024].  dtype is
+// a llmint8_dtype.  rows_out >= R: scales of rows [R, rows_out) are written as zero (R, or R
+// rounded up to 128 where the whole buffer is to be defined).
+cudaError_t launch_mxfp4_quantize(const void *X, int dtype, int64_t ldx, int64_t R,
+                                  int64_t rows_out, int64_t K, uint8_t *codes, uint8_t *scales,
+                                  cudaStream_t s);
+cudaError_t launch_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t R,
+                                 int64_t K, void *out, int dtype, cudaStream_t s);
+
+// The MXFP4 product (gemm_mxfp4.cu).
+struct Mxfp4Gemm {
+    const uint8_t *Xc, *Xs;  // X [M, K]
+    const uint8_t *Wc, *Ws;  // W [N, K]
+    const void *bias;        // [N] or null
+    void *Y;                 // [M, N]
+    int dtype;               // of bias and Y
+    int weights_ready;       // W does not depend on the kernel launched last on the stream
+    StatusRef status;
+    int64_t M, N, K;
+    uint64_t timeout_ns;
+};
+cudaError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, cudaStream_t s);
+
+// The residual norm (norm.cu).
+constexpr int64_t kNormMaxK = 32768;
+struct NormArgs {
+    const void *X, *residual;            // [M, K], row pitches ldx, ldr; residual may be null
+    const void *post_weight, *post_bias; // [K] or null
+    const void *gate;                    // [M / gate_group, K] or null
+    const void *weight, *bias;           // [K] or null
+    void *H, *Y;                         // [M, K] or null
+    uint8_t *codes, *scales;             // y as MXFP4, or null
+    int64_t M, K, ldx, ldr;
+    int64_t gate_group;                  // rows that share a row of the gate
+    int64_t rows_out, tiles_k;           // of the scales
+    int norm, post_norm;                 // llmint8_norm
+    float scale, eps;
+};
+cudaError_t launch_residual_norm(const NormArgs &a, int dtype, cudaStream_t s);
+
+}  // namespace llmint8

@@ -1,0 +1,183 @@
+// What stands between two blocks of a transformer, in one pass over the rows:
+//     h = residual + scale * gate * PostNorm(x)
+//     y = Norm(h)
+// where a norm is v / sqrt(mean(v^2) + eps) * w + b ("rms") or the same of v - mean(v) ("layer"),
+// both norms, the residual and the gate are optional, and y leaves as 16-bit values, as an MXFP4
+// operand for the product that follows, or both.
+//
+// Bound by HBM: x and the residual are read once, h and y written once.  So a row stays in the
+// registers of its threads (8 elements to a chunk, up to 4 chunks a thread, 32 to 1024 threads a
+// row) from its loads to its stores, and each sum over the row is a shuffle tree and one exchange
+// through shared memory.  All arithmetic is fp32; h and y are each rounded once, y from the
+// unrounded h, and the MXFP4 form is that of the rounded y, so that it is bit for bit what
+// quantising the stored y gives.  A layer norm's variance is the mean of (v - mean)^2, summed
+// after the mean is known: the difference of mean squares would cancel.
+#include "kernels.h"
+#include "launch.cuh"
+#include "mxfp4.cuh"
+
+namespace llmint8 {
+
+namespace {
+
+constexpr int kMaxWarps = 32;
+
+// Sum over the `tpr` threads of this row (a power of two, 32 to 1024); every thread of the CTA
+// takes part.  `red` has one slot per warp, and two calls in turn use two sets of them.
+__device__ __forceinline__ float row_sum(float v, float *red, int tpr) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (tpr == 32) return v;
+    const int warp = threadIdx.x >> 5, wpr = tpr >> 5;
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    // lane l takes warp l of the row, so that every thread adds in the same order
+    const int l = threadIdx.x & 31;
+    v = l < wpr ? red[(warp & ~(wpr - 1)) + l] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// Norm factors of a row held as NCH chunks of 8 (zero outside the row): mean and 1 / deviation.
+template <int NCH>
+__device__ __forceinline__ void row_norm(const float (&v)[NCH][8], const bool (&in)[NCH], int kind,
+                                         float inv_k, float eps, float *red, int tpr, float &mean,
+                                         float &rstd) {
+    mean = 0.0f;
+    if (kind == LLMINT8_NORM_LAYER) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s += v[i][e];
+        mean = row_sum(s, red, tpr) * inv_k;
+    }
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i)
+        if (in[i]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = fmaf(v[i][e] - mean, v[i][e] - mean, q);
+        }
+    rstd = rsqrtf(row_sum(q, red + kMaxWarps, tpr) * inv_k + eps);
+}
+
+// v = (v - mean) * rstd * w + b over one chunk; w and b may be null.
+template <int DT>
+__device__ __forceinline__ void apply_norm(float (&v)[8], float mean, float rstd, const void *w,
+                                           const void *b, int64_t ch) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * rstd;
+    float t[8];
+    if (w) {
+        unpack_chunk<DT>(load_chunk<DT>(w, ch), t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= t[e];
+    }
+    if (b) {
+        unpack_chunk<DT>(load_chunk<DT>(b, ch), t);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += t[e];
+    }
+}
+
+template <int DT, int NCH>
+__global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a, int tpr_log2) {
+    pdl_wait_then_release();
+    __shared__ float red[4 * kMaxWarps];
+    const int tpr = 1 << tpr_log2;
+    const int t = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
+    const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> tpr_log2) + (threadIdx.x >> tpr_log2);
+    const bool live = row < a.M;
+    const int64_t chunks = a.K / 8;
+    const float inv_k = 1.0f / (float)a.K;
+
+    const uint8_t *xr = static_cast<const uint8_t *>(a.X) + (live ? row : 0) * a.ldx * 2;
+    const uint8_t *rr =
+        a.residual ? static_cast<const uint8_t *>(a.residual) + (live ? row : 0) * a.ldr * 2
+                   : nullptr;
+    Chunk<DT> x[NCH], r[NCH];
+    bool in[NCH];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {      // issue every load before using any
+        const int64_t ch = t + ((int64_t)i << tpr_log2);
+        in[i] = live && ch < chunks;
+        x[i] = in[i] ? load_chunk<DT>(xr, ch) : zero_chunk<DT>();
+        r[i] = in[i] && rr ? load_chunk<DT>(rr, ch) : zero_chunk<DT>();
+    }
+    float h[NCH][8];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) unpack_chunk<DT>(x[i], h[i]);
+    float mean, rstd;
+    if (a.post_norm != LLMINT8_NORM_NONE) {
+        row_norm<NCH>(h, in, a.post_norm, inv_k, a.eps, red, tpr, mean, rstd);
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+            if (in[i])
+                apply_norm<DT>(h[i], mean, rstd, a.post_weight, a.post_bias,
+                               t + ((int64_t)i << tpr_log2));
+    }
+    const uint8_t *gr = a.gate ? static_cast<const uint8_t *>(a.gate) +
+                                     (live ? row / a.gate_group : 0) * a.K * 2
+                               : nullptr;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        if (!in[i]) continue;
+        const int64_t ch = t + ((int64_t)i << tpr_log2);
+        float u[8];
+        if (gr) {
+            unpack_chunk<DT>(load_chunk<DT>(gr, ch), u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[i][e] *= u[e];
+        }
+        unpack_chunk<DT>(r[i], u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[i][e] = fmaf(h[i][e], a.scale, u[e]);
+        if (a.H) store_chunk<DT>(static_cast<uint8_t *>(a.H) + row * a.K * 2, ch,
+                                 pack_chunk<DT>(h[i]));
+    }
+    if (a.norm == LLMINT8_NORM_NONE) return;   // uniform over the grid
+    row_norm<NCH>(h, in, a.norm, inv_k, a.eps, red + 2 * kMaxWarps, tpr, mean, rstd);
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        const int64_t ch = t + ((int64_t)i << tpr_log2);
+        Chunk<DT> y = zero_chunk<DT>();
+        if (in[i]) {
+            apply_norm<DT>(h[i], mean, rstd, a.weight, a.bias, ch);
+            y = pack_chunk<DT>(h[i]);
+            if (a.Y) store_chunk<DT>(static_cast<uint8_t *>(a.Y) + row * a.K * 2, ch, y);
+        }
+        // a warp's 32 chunks are one row's share of a scale tile; rows past M pad the last one
+        if (a.codes && row < a.rows_out && (ch >> 5) < a.tiles_k)
+            quantize_tile_row<DT>(y, in[i], row, ch >> 5, chunks, a.tiles_k,
+                                  reinterpret_cast<uint32_t *>(a.codes), a.scales, lane);
+    }
+}
+
+template <int DT>
+cudaError_t norm_launch(const NormArgs &a, cudaStream_t s) {
+    // Threads to a row: enough for at most 4 chunks each; while the grid is small, one chunk each,
+    // since a lone row's time is its chain of latencies.
+    const int64_t chunks = ceil_div(a.K, kMxCols) * 32;
+    const int want = a.M <= 148 ? 1 : 2;
+    int tpr_log2 = 5;
+    while (tpr_log2 < 10 && ((int64_t)want << tpr_log2) < chunks) ++tpr_log2;
+    const int64_t per = ceil_div(chunks, (int64_t)1 << tpr_log2);
+    const int threads = std::max(1 << tpr_log2, 128);
+    const int64_t rows = a.codes ? a.rows_out : a.M;
+    const dim3 grid((unsigned)ceil_div(rows, threads >> tpr_log2));
+    if (per <= 1) return launch_pdl(residual_norm_kernel<DT, 1>, grid, dim3(threads), s, a, tpr_log2);
+    if (per <= 2) return launch_pdl(residual_norm_kernel<DT, 2>, grid, dim3(threads), s, a, tpr_log2);
+    return launch_pdl(residual_norm_kernel<DT, 4>, grid, dim3(threads), s, a, tpr_log2);
+}
+
+}  // namespace
+
+cudaError_t launch_residual_norm(const NormArgs &a, int dtype, cudaStream_t s) {
+    const cudaError_t e = dtype == kF16 ? norm_launch<kF16>(a, s) : norm_launch<kBF16>(a, s);
+    note_launches(1);
+    return e;
+}
+
+}  // namespace llmint8

@@ -12,21 +12,13 @@
 // product rounded once to fp32, then round-half-to-even to an integer.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.cuh"
 
 namespace llmint8 {
 
 namespace {
 
 constexpr int kThreads = 256;
-
-// Programmatic dependent launch: every kernel of a layer call is launched so that its CTAs
-// may start while the previous kernel in the stream finishes.  Each waits for that kernel
-// (and so for everything before it) before it touches global memory, and lets the next one
-// launch right away.
-__device__ __forceinline__ void pdl_wait_then_release() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
     const __half2 *h = reinterpret_cast<const __half2 *>(&v);
@@ -471,27 +463,6 @@ ScanPlan scan_plan(int64_t M, int64_t K) {
     p.nwords = ceil_div(K, 32);
     return p;
 }
-
-namespace {
-
-// Launch with the programmatic-stream-serialization attribute (see pdl_wait_then_release).
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, cudaStream_t s,
-                       Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = 0;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-}  // namespace
 
 cudaError_t launch_outlier_detect(const __half *X, int64_t M, int64_t K, float threshold,
                                   const ScanPlan &plan, uint32_t *partial, uint32_t *bitmap,

@@ -7,6 +7,7 @@ fallback: a missing library raises ``LLMInt8LibraryError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -59,6 +60,17 @@ PROTOTYPES = {
                                                          _P]),
     "llmint8_linear_with_bitmaps": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _I64,
                                                    _I64, _P, _P, _SZ, _P, _P]),
+    "llmint8_mxfp4_scales_size": (_SZ, [_I64, _I64]),
+    "llmint8_mxfp4_quantize": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _P]),
+    "llmint8_mxfp4_dequant": (ctypes.c_int, [_P, _P, _I64, _I64, _P, ctypes.c_int, _P]),
+    "llmint8_mxfp4_linear": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _P, _I64, _P,
+                                            _P, _P, _SZ, _P]),
+    "llmint8_mxfp4_linear_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "llmint8_mxfp4_linear_quantized": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P,
+                                                      ctypes.c_int, _P, _SZ, _P]),
+    "llmint8_residual_norm": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _P, _I64,
+                                             ctypes.c_int, _P, _P, _P, _I64, _F32, ctypes.c_int,
+                                             _P, _P, _F32, _P, _P, _P, _P, _P]),
 }
 
 
@@ -509,3 +521,269 @@ def llmint8_linear_noalloc(X: torch.Tensor, CB: torch.Tensor, SCB: torch.Tensor,
                                          ctypes.byref(scratch)),
            "llmint8_linear_noalloc")
     return int(scratch.value or 0)
+
+
+# ------------------------------------------------------------ MXFP4 and the residual norm ---
+#
+# Unlike the calls above, these take tensors of any CUDA device (all of one; it need not be the
+# current one), rows of any pitch that is a multiple of 16 bytes where a matrix of values goes in,
+# and no rows at all (M = 0 returns empty outputs).  With `stream`, outputs and workspaces made
+# here belong to that stream.
+
+DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}     # llmint8_dtype
+NORMS = {None: 0, "rms": 1, "layer": 2}                              # llmint8_norm
+_DTYPES16 = (torch.float16, torch.bfloat16)
+_MX_HEADER = 256          # bytes of a workspace that holds a status alone
+
+
+@contextlib.contextmanager
+def _running_on(device: torch.device, stream):
+    """The device, and the stream when one is given, made current."""
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            yield _stream(None)
+
+
+def _rows(t: torch.Tensor, dtypes, name: str):
+    """(address, row pitch in elements) of a matrix of values whose rows are contiguous."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError("llmint8 tensors must live on a CUDA device")
+    M, K = t.shape
+    ld = t.stride(0) if M > 1 else K
+    if K > 1 and t.stride(1) != 1 or ld < K or ld * t.element_size() % 16 or t.data_ptr() % 16:
+        raise ValueError(f"{name}'s rows must be contiguous and start on 16 bytes each, got "
+                         f"strides {tuple(t.stride())}")
+    return ctypes.c_void_p(t.data_ptr()), ld
+
+
+def _arg(t: torch.Tensor | None, dtype: torch.dtype, shape, name: str, device: torch.device):
+    """Address of a dense argument or output, or None."""
+    if t is None:
+        return None
+    _want(t, dtype, shape, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+    return _ptr(t)
+
+
+def mxfp4_scales_shape(R: int, K: int) -> tuple[int, int, int]:
+    """Shape of the scales of an MXFP4 matrix of R rows and K columns (tiles of 128 x 256)."""
+    return (R + 127) // 128, (K + 255) // 256, 1024
+
+
+def mxfp4_tile_scales(scales: torch.Tensor) -> torch.Tensor:
+    """Scale bytes in plain order, uint8 [R, K/32], in the tiled layout that the MXFP4 calls take
+    (a change of layout, done once for a weight that was quantized elsewhere)."""
+    if scales.dtype != torch.uint8 or scales.dim() != 2:
+        raise ValueError("scales must be uint8 [R, K/32]")
+    R, B = scales.shape
+    rt, kt, _ = mxfp4_scales_shape(R, 32 * B)
+    padded = torch.zeros((rt * 128, kt * 8), dtype=torch.uint8, device=scales.device)
+    padded[:R, :B] = scales
+    return padded.view(rt, 4, 32, kt, 2, 4).permute(0, 3, 4, 2, 1, 5).reshape(rt, kt, 1024)
+
+
+def mxfp4_untile_scales(scales: torch.Tensor, R: int, K: int) -> torch.Tensor:
+    """The inverse of mxfp4_tile_scales: uint8 [R, K/32] in plain order."""
+    rt, kt, _ = mxfp4_scales_shape(R, K)
+    _want(scales, torch.uint8, (rt, kt, 1024), "scales")
+    plain = scales.view(rt, kt, 2, 32, 4, 4).permute(0, 4, 3, 1, 2, 5).reshape(rt * 128, kt * 8)
+    return plain[:R, :K // 32]
+
+
+def llmint8_mxfp4_scales_size(R: int, K: int) -> int:
+    return int(load().llmint8_mxfp4_scales_size(R, K))
+
+
+def llmint8_mxfp4_linear_workspace_size(M: int, N: int, K: int) -> int:
+    return int(load().llmint8_mxfp4_linear_workspace_size(M, N, K))
+
+
+def llmint8_mxfp4_quantize(X: torch.Tensor, codes=None, scales=None, stream=None):
+    """X fp16, bf16 or fp32 [R, K] (a weight or activations) -> MXFP4: (codes uint8 [R, K/2],
+    scales uint8 [ceil(R/128), ceil(K/256), 1024])."""
+    px, ld = _rows(X, tuple(DTYPES), "X")
+    R, K = X.shape
+    dev = X.device
+    with _running_on(dev, stream) as s:
+        if codes is None:
+            codes = torch.empty((R, K // 2), dtype=torch.uint8, device=dev)
+        if scales is None:
+            scales = torch.empty(mxfp4_scales_shape(R, K), dtype=torch.uint8, device=dev)
+        _check(load().llmint8_mxfp4_quantize(
+            px, DTYPES[X.dtype], R, K, ld, _arg(codes, torch.uint8, (R, K // 2), "codes", dev),
+            _arg(scales, torch.uint8, mxfp4_scales_shape(R, K), "scales", dev), s),
+            "llmint8_mxfp4_quantize")
+    return codes, scales
+
+
+def llmint8_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor,
+                          dtype: torch.dtype = torch.float16, out=None, stream=None):
+    """The values of an MXFP4 matrix, [R, K] of `dtype` (fp16, bf16 or fp32)."""
+    R, K = codes.shape[0], 2 * codes.shape[1]
+    dev = codes.device
+    if dtype not in DTYPES:
+        raise TypeError(f"dtype must be one of {', '.join(map(str, DTYPES))}, got {dtype}")
+    pc = _arg(codes, torch.uint8, (R, K // 2), "codes", dev)
+    ps = _arg(scales, torch.uint8, mxfp4_scales_shape(R, K), "scales", dev)
+    with _running_on(dev, stream) as s:
+        out = torch.empty((R, K), dtype=dtype, device=dev) if out is None else out
+        _check(load().llmint8_mxfp4_dequant(pc, ps, R, K, _arg(out, dtype, (R, K), "out", dev),
+                                            DTYPES[dtype], s), "llmint8_mxfp4_dequant")
+    return out
+
+
+def _mxfp4_weight(WC: torch.Tensor, WS: torch.Tensor, K: int, dev: torch.device):
+    N = WC.shape[0]
+    return (N, _arg(WC, torch.uint8, (N, K // 2), "WC", dev),
+            _arg(WS, torch.uint8, mxfp4_scales_shape(N, K), "WS", dev))
+
+
+def _workspace(workspace, need: int, dev: torch.device):
+    if workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev:
+        raise ValueError(f"the workspace must be uint8 on {dev}")
+    return workspace
+
+
+def llmint8_mxfp4_linear(X: torch.Tensor, WC: torch.Tensor, WS: torch.Tensor, bias=None, Y=None,
+                         workspace=None, stream=None):
+    """The MXFP4 layer: Y [M, N] from X [M, K] (fp16 or bf16, quantized in the call) and the weight
+    (WC, WS) of llmint8_mxfp4_quantize; bias and Y are of X's type."""
+    px, ld = _rows(X, _DTYPES16, "X")
+    M, K = X.shape
+    dev = X.device
+    N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
+    pb = _arg(bias, X.dtype, (N,), "bias", dev)
+    with _running_on(dev, stream) as s:
+        Y = torch.empty((M, N), dtype=X.dtype, device=dev) if Y is None else Y
+        ws = _workspace(workspace, llmint8_mxfp4_linear_workspace_size(M, N, K), dev)
+        _check(load().llmint8_mxfp4_linear(px, DTYPES[X.dtype], M, K, ld, pc, ps, N, pb,
+                                           _arg(Y, X.dtype, (M, N), "Y", dev), _ptr(ws),
+                                           ws.numel(), s), "llmint8_mxfp4_linear")
+    return Y
+
+
+def llmint8_mxfp4_linear_quantized(XC: torch.Tensor, XS: torch.Tensor, WC: torch.Tensor,
+                                   WS: torch.Tensor, bias=None, dtype: torch.dtype = torch.float16,
+                                   Y=None, workspace=None, stream=None):
+    """The MXFP4 layer on an X that is MXFP4 already (llmint8_mxfp4_quantize's or
+    llmint8_residual_norm_mxfp4's): Y [M, N] of `dtype` (fp16 or bf16)."""
+    M, K = XC.shape[0], 2 * XC.shape[1]
+    dev = XC.device
+    if dtype not in _DTYPES16:
+        raise TypeError(f"dtype must be one of {', '.join(map(str, _DTYPES16))}, got {dtype}")
+    xc = _arg(XC, torch.uint8, (M, K // 2), "XC", dev)
+    xs = _arg(XS, torch.uint8, mxfp4_scales_shape(M, K), "XS", dev)
+    N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
+    pb = _arg(bias, dtype, (N,), "bias", dev)
+    with _running_on(dev, stream) as s:
+        Y = torch.empty((M, N), dtype=dtype, device=dev) if Y is None else Y
+        ws = _workspace(workspace, _MX_HEADER, dev)
+        _check(load().llmint8_mxfp4_linear_quantized(xc, xs, M, K, pc, ps, N, pb,
+                                                     _arg(Y, dtype, (M, N), "Y", dev),
+                                                     DTYPES[dtype], _ptr(ws), ws.numel(), s),
+               "llmint8_mxfp4_linear_quantized")
+    return Y
+
+
+class Mxfp4LinearPlan:
+    """One llmint8_mxfp4_linear call with its arguments checked and marshalled once (as
+    LinearPlan for the int8 layer): calling the plan runs the layer on the same tensors, which
+    must stay alive and keep their storage while the plan is used.  Made with the tensors' device
+    current, and called with it current."""
+
+    def __init__(self, X: torch.Tensor, WC: torch.Tensor, WS: torch.Tensor, bias=None, Y=None,
+                 workspace=None, stream=None):
+        px, ld = _rows(X, _DTYPES16, "X")
+        M, K = X.shape
+        dev = X.device
+        N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
+        pb = _arg(bias, X.dtype, (N,), "bias", dev)
+        with _running_on(dev, stream) as s:
+            self.Y = torch.empty((M, N), dtype=X.dtype, device=dev) if Y is None else Y
+            self.workspace = _workspace(workspace, llmint8_mxfp4_linear_workspace_size(M, N, K),
+                                        dev)
+        self._keep = (X, WC, WS, bias, stream)
+        self._fn = load().llmint8_mxfp4_linear
+        self._args = (px, DTYPES[X.dtype], M, K, ld, pc, ps, N, pb,
+                      _arg(self.Y, X.dtype, (M, N), "Y", dev), _ptr(self.workspace),
+                      self.workspace.numel(), s)
+
+    def __call__(self) -> torch.Tensor:
+        code = self._fn(*self._args)
+        if code != OK:
+            raise LLMInt8Error(code, "llmint8_mxfp4_linear")
+        return self.Y
+
+
+def _residual_norm(X, residual, weight, bias, norm, post_norm, post_weight, post_bias, gate, scale,
+                   eps, H, Y, codes, scales, want_y, want_codes, stream):
+    px, ld = _rows(X, _DTYPES16, "X")
+    M, K = X.shape
+    dev, dt = X.device, X.dtype
+    if norm not in NORMS or post_norm not in NORMS:
+        raise ValueError(f"norm and post_norm are one of {', '.join(map(repr, NORMS))}")
+    pr, ldr = (None, K) if residual is None else _rows(residual, (dt,), "residual")
+    if residual is not None and (residual.shape != X.shape or residual.device != dev):
+        raise ValueError("residual must have X's shape and device")
+    G = 1
+    if gate is not None:
+        G = gate.shape[0] if gate.dim() == 2 else 1
+        if gate.dim() == 1:
+            gate = gate.view(1, -1)
+        if G < 1 or M % G:
+            raise ValueError(f"the gate's {G} rows must divide X's {M}")
+    vec = lambda t, name: _arg(t, dt, (K,), name, dev)  # noqa: E731
+    shape = mxfp4_scales_shape(M, K)
+    with _running_on(dev, stream) as s:
+        H = torch.empty((M, K), dtype=dt, device=dev) if H is None else H
+        if want_y:
+            Y = torch.empty((M, K), dtype=dt, device=dev) if Y is None else Y
+        if want_codes:
+            codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev) if codes is None \
+                else codes
+            scales = torch.empty(shape, dtype=torch.uint8, device=dev) if scales is None \
+                else scales
+        _check(load().llmint8_residual_norm(
+            px, DTYPES[dt], M, K, ld, pr, ldr, NORMS[post_norm], vec(post_weight, "post_weight"),
+            vec(post_bias, "post_bias"), _arg(gate, dt, (G, K), "gate", dev), G,
+            ctypes.c_float(scale), NORMS[norm], vec(weight, "weight"), vec(bias, "bias"),
+            ctypes.c_float(eps), _arg(H, dt, (M, K), "H", dev), _arg(Y, dt, (M, K), "Y", dev),
+            _arg(codes, torch.uint8, (M, K // 2), "codes", dev),
+            _arg(scales, torch.uint8, shape, "scales", dev), s), "llmint8_residual_norm")
+    return H, Y, codes, scales
+
+
+def llmint8_residual_norm(X: torch.Tensor, residual=None, weight=None, bias=None,
+                          norm: str | None = "rms", post_norm: str | None = None,
+                          post_weight=None, post_bias=None, gate=None, scale: float = 1.0,
+                          eps: float = 1e-6, H=None, Y=None, stream=None):
+    """The step between two blocks: H = residual + scale * gate * PostNorm(X), Y = Norm(H); returns
+    (H, Y), both [M, K] of X's type (fp16 or bf16).  norm and post_norm are "rms", "layer" or None
+    (norm=None: Y is None); gate is [K] or [G, K], row m taking gate row m // (M // G).  H may be
+    the residual's own buffer."""
+    return _residual_norm(X, residual, weight, bias, norm, post_norm, post_weight, post_bias, gate,
+                          scale, eps, H, Y, None, None, norm is not None, False, stream)[:2]
+
+
+def llmint8_residual_norm_mxfp4(X: torch.Tensor, residual=None, weight=None, bias=None,
+                                norm: str = "rms", post_norm: str | None = None,
+                                post_weight=None, post_bias=None, gate=None, scale: float = 1.0,
+                                eps: float = 1e-6, H=None, codes=None, scales=None, stream=None):
+    """llmint8_residual_norm whose Y leaves as MXFP4 for llmint8_mxfp4_linear_quantized (bit for
+    bit the quantized Y): returns (H, codes, scales)."""
+    H, _, codes, scales = _residual_norm(X, residual, weight, bias, norm, post_norm, post_weight,
+                                         post_bias, gate, scale, eps, H, None, codes, scales,
+                                         False, True, stream)
+    return H, codes, scales
