@@ -7,8 +7,8 @@ fallback: a missing library raises ``LLMInt8LibraryError``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -91,6 +91,8 @@ def library_path() -> str:
 def load():
     """The ctypes handle of libllmint8.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -536,21 +538,24 @@ _DTYPES16 = (torch.float16, torch.bfloat16)
 _MX_HEADER = 256          # bytes of a workspace that holds a status alone
 
 
-@contextlib.contextmanager
-def _running_on(device: torch.device, stream):
-    """The device, and the stream when one is given, made current."""
+def _run(device: torch.device, stream, call):
+    """call(raw stream), with the device - and the stream, when one is given - current."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            yield _stream(None)
+            return call(stream.cuda_stream)
+    # the handle alone: a Stream object for it costs 3 us, a third of a small call
+    index = device.index
+    if index == torch.cuda.current_device():
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(device):
+        return call(torch._C._cuda_getCurrentRawStream(index))
 
 
 def _rows(t: torch.Tensor, dtypes, name: str):
-    """(address, row pitch in elements) of a matrix of values whose rows are contiguous."""
+    """(rows, columns, address, row pitch in elements) of a matrix of values whose rows are
+    contiguous."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
     if t.dim() != 2:
@@ -558,21 +563,27 @@ def _rows(t: torch.Tensor, dtypes, name: str):
     if not t.is_cuda:
         raise ValueError("llmint8 tensors must live on a CUDA device")
     M, K = t.shape
-    ld = t.stride(0) if M > 1 else K
-    if K > 1 and t.stride(1) != 1 or ld < K or ld * t.element_size() % 16 or t.data_ptr() % 16:
+    ld, one = t.stride()
+    if M <= 1:
+        ld = K
+    at = t.data_ptr()
+    if (one != 1 and K > 1) or ld < K or ld * t.element_size() % 16 or at % 16:
         raise ValueError(f"{name}'s rows must be contiguous and start on 16 bytes each, got "
                          f"strides {tuple(t.stride())}")
-    return ctypes.c_void_p(t.data_ptr()), ld
+    return M, K, at, ld
 
 
 def _arg(t: torch.Tensor | None, dtype: torch.dtype, shape, name: str, device: torch.device):
     """Address of a dense argument or output, or None."""
     if t is None:
         return None
-    _want(t, dtype, shape, name)
+    if t.dtype != dtype or t.shape != shape:
+        _want(t, dtype, shape, name)
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError("llmint8 tensors must be contiguous")
+    return t.data_ptr()
 
 
 def mxfp4_scales_shape(R: int, K: int) -> tuple[int, int, int]:
@@ -604,6 +615,7 @@ def llmint8_mxfp4_scales_size(R: int, K: int) -> int:
     return int(load().llmint8_mxfp4_scales_size(R, K))
 
 
+@functools.lru_cache(maxsize=4096)
 def llmint8_mxfp4_linear_workspace_size(M: int, N: int, K: int) -> int:
     return int(load().llmint8_mxfp4_linear_workspace_size(M, N, K))
 
@@ -611,67 +623,82 @@ def llmint8_mxfp4_linear_workspace_size(M: int, N: int, K: int) -> int:
 def llmint8_mxfp4_quantize(X: torch.Tensor, codes=None, scales=None, stream=None):
     """X fp16, bf16 or fp32 [R, K] (a weight or activations) -> MXFP4: (codes uint8 [R, K/2],
     scales uint8 [ceil(R/128), ceil(K/256), 1024])."""
-    px, ld = _rows(X, tuple(DTYPES), "X")
-    R, K = X.shape
+    R, K, px, ld = _rows(X, DTYPES, "X")
     dev = X.device
-    with _running_on(dev, stream) as s:
-        if codes is None:
-            codes = torch.empty((R, K // 2), dtype=torch.uint8, device=dev)
-        if scales is None:
-            scales = torch.empty(mxfp4_scales_shape(R, K), dtype=torch.uint8, device=dev)
+    c_shape, s_shape = (R, K // 2), mxfp4_scales_shape(R, K)
+
+    def call(s):
+        c = X.new_empty(c_shape, dtype=torch.uint8) if codes is None else codes
+        t = X.new_empty(s_shape, dtype=torch.uint8) if scales is None else scales
         _check(load().llmint8_mxfp4_quantize(
-            px, DTYPES[X.dtype], R, K, ld, _arg(codes, torch.uint8, (R, K // 2), "codes", dev),
-            _arg(scales, torch.uint8, mxfp4_scales_shape(R, K), "scales", dev), s),
-            "llmint8_mxfp4_quantize")
-    return codes, scales
+            px, DTYPES[X.dtype], R, K, ld, _arg(c, torch.uint8, c_shape, "codes", dev),
+            _arg(t, torch.uint8, s_shape, "scales", dev), s), "llmint8_mxfp4_quantize")
+        return c, t
+    return _run(dev, stream, call)
 
 
 def llmint8_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor,
                           dtype: torch.dtype = torch.float16, out=None, stream=None):
     """The values of an MXFP4 matrix, [R, K] of `dtype` (fp16, bf16 or fp32)."""
-    R, K = codes.shape[0], 2 * codes.shape[1]
-    dev = codes.device
+    R, K, dev, pc, ps = _mxfp4_matrix(codes, scales, "codes", "scales")
     if dtype not in DTYPES:
         raise TypeError(f"dtype must be one of {', '.join(map(str, DTYPES))}, got {dtype}")
-    pc = _arg(codes, torch.uint8, (R, K // 2), "codes", dev)
-    ps = _arg(scales, torch.uint8, mxfp4_scales_shape(R, K), "scales", dev)
-    with _running_on(dev, stream) as s:
-        out = torch.empty((R, K), dtype=dtype, device=dev) if out is None else out
-        _check(load().llmint8_mxfp4_dequant(pc, ps, R, K, _arg(out, dtype, (R, K), "out", dev),
+
+    def call(s):
+        v = codes.new_empty((R, K), dtype=dtype) if out is None else out
+        _check(load().llmint8_mxfp4_dequant(pc, ps, R, K, _arg(v, dtype, (R, K), "out", dev),
                                             DTYPES[dtype], s), "llmint8_mxfp4_dequant")
-    return out
+        return v
+    return _run(dev, stream, call)
+
+
+def _mxfp4_matrix(codes: torch.Tensor, scales: torch.Tensor, c_name: str, s_name: str):
+    """(rows, columns, device, address of the codes, of the scales) of an MXFP4 matrix."""
+    if codes.dim() != 2:
+        raise ValueError(f"{c_name} must have two dimensions, got {tuple(codes.shape)}")
+    if not codes.is_cuda:
+        raise ValueError("llmint8 tensors must live on a CUDA device")
+    R, half = codes.shape
+    dev = codes.device
+    return (R, 2 * half, dev, _arg(codes, torch.uint8, (R, half), c_name, dev),
+            _arg(scales, torch.uint8, mxfp4_scales_shape(R, 2 * half), s_name, dev))
 
 
 def _mxfp4_weight(WC: torch.Tensor, WS: torch.Tensor, K: int, dev: torch.device):
-    N = WC.shape[0]
-    return (N, _arg(WC, torch.uint8, (N, K // 2), "WC", dev),
-            _arg(WS, torch.uint8, mxfp4_scales_shape(N, K), "WS", dev))
+    """(rows, address of the codes, of the scales) of a layer's weight."""
+    N, k, d, pc, ps = _mxfp4_matrix(WC, WS, "WC", "WS")
+    if k != K or d != dev:
+        raise ValueError(f"the weight has {k} columns on {d}, X {K} on {dev}")
+    return N, pc, ps
 
 
-def _workspace(workspace, need: int, dev: torch.device):
-    if workspace is None:
-        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    if workspace.dtype != torch.uint8 or workspace.device != dev:
-        raise ValueError(f"the workspace must be uint8 on {dev}")
+def _workspace(workspace, dev: torch.device):
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be dense uint8 on {dev}")
     return workspace
+
+
+def _linear_args(X, WC, WS, bias, Y, workspace, s):
+    """(Y, workspace, the C call's arguments) of an MXFP4 layer on raw stream s."""
+    M, K, px, ld = _rows(X, _DTYPES16, "X")
+    dev, dt = X.device, X.dtype
+    N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
+    Y = X.new_empty((M, N)) if Y is None else Y
+    ws = WC.new_empty((llmint8_mxfp4_linear_workspace_size(M, N, K),)) if workspace is None \
+        else _workspace(workspace, dev)
+    return Y, ws, (px, DTYPES[dt], M, K, ld, pc, ps, N, _arg(bias, dt, (N,), "bias", dev),
+                   _arg(Y, dt, (M, N), "Y", dev), ws.data_ptr(), ws.numel(), s)
 
 
 def llmint8_mxfp4_linear(X: torch.Tensor, WC: torch.Tensor, WS: torch.Tensor, bias=None, Y=None,
                          workspace=None, stream=None):
     """The MXFP4 layer: Y [M, N] from X [M, K] (fp16 or bf16, quantized in the call) and the weight
     (WC, WS) of llmint8_mxfp4_quantize; bias and Y are of X's type."""
-    px, ld = _rows(X, _DTYPES16, "X")
-    M, K = X.shape
-    dev = X.device
-    N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
-    pb = _arg(bias, X.dtype, (N,), "bias", dev)
-    with _running_on(dev, stream) as s:
-        Y = torch.empty((M, N), dtype=X.dtype, device=dev) if Y is None else Y
-        ws = _workspace(workspace, llmint8_mxfp4_linear_workspace_size(M, N, K), dev)
-        _check(load().llmint8_mxfp4_linear(px, DTYPES[X.dtype], M, K, ld, pc, ps, N, pb,
-                                           _arg(Y, X.dtype, (M, N), "Y", dev), _ptr(ws),
-                                           ws.numel(), s), "llmint8_mxfp4_linear")
-    return Y
+    def call(s):
+        out, ws, args = _linear_args(X, WC, WS, bias, Y, workspace, s)
+        _check(load().llmint8_mxfp4_linear(*args), "llmint8_mxfp4_linear")
+        return out
+    return _run(X.device, stream, call)
 
 
 def llmint8_mxfp4_linear_quantized(XC: torch.Tensor, XS: torch.Tensor, WC: torch.Tensor,
@@ -679,22 +706,21 @@ def llmint8_mxfp4_linear_quantized(XC: torch.Tensor, XS: torch.Tensor, WC: torch
                                    Y=None, workspace=None, stream=None):
     """The MXFP4 layer on an X that is MXFP4 already (llmint8_mxfp4_quantize's or
     llmint8_residual_norm_mxfp4's): Y [M, N] of `dtype` (fp16 or bf16)."""
-    M, K = XC.shape[0], 2 * XC.shape[1]
-    dev = XC.device
     if dtype not in _DTYPES16:
         raise TypeError(f"dtype must be one of {', '.join(map(str, _DTYPES16))}, got {dtype}")
-    xc = _arg(XC, torch.uint8, (M, K // 2), "XC", dev)
-    xs = _arg(XS, torch.uint8, mxfp4_scales_shape(M, K), "XS", dev)
+    M, K, dev, xc, xs = _mxfp4_matrix(XC, XS, "XC", "XS")
     N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
     pb = _arg(bias, dtype, (N,), "bias", dev)
-    with _running_on(dev, stream) as s:
-        Y = torch.empty((M, N), dtype=dtype, device=dev) if Y is None else Y
-        ws = _workspace(workspace, _MX_HEADER, dev)
+
+    def call(s):
+        out = XC.new_empty((M, N), dtype=dtype) if Y is None else Y
+        ws = XC.new_empty((_MX_HEADER,)) if workspace is None else _workspace(workspace, dev)
         _check(load().llmint8_mxfp4_linear_quantized(xc, xs, M, K, pc, ps, N, pb,
-                                                     _arg(Y, dtype, (M, N), "Y", dev),
-                                                     DTYPES[dtype], _ptr(ws), ws.numel(), s),
+                                                     _arg(out, dtype, (M, N), "Y", dev),
+                                                     DTYPES[dtype], ws.data_ptr(), ws.numel(), s),
                "llmint8_mxfp4_linear_quantized")
-    return Y
+        return out
+    return _run(dev, stream, call)
 
 
 class Mxfp4LinearPlan:
@@ -705,20 +731,10 @@ class Mxfp4LinearPlan:
 
     def __init__(self, X: torch.Tensor, WC: torch.Tensor, WS: torch.Tensor, bias=None, Y=None,
                  workspace=None, stream=None):
-        px, ld = _rows(X, _DTYPES16, "X")
-        M, K = X.shape
-        dev = X.device
-        N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
-        pb = _arg(bias, X.dtype, (N,), "bias", dev)
-        with _running_on(dev, stream) as s:
-            self.Y = torch.empty((M, N), dtype=X.dtype, device=dev) if Y is None else Y
-            self.workspace = _workspace(workspace, llmint8_mxfp4_linear_workspace_size(M, N, K),
-                                        dev)
         self._keep = (X, WC, WS, bias, stream)
         self._fn = load().llmint8_mxfp4_linear
-        self._args = (px, DTYPES[X.dtype], M, K, ld, pc, ps, N, pb,
-                      _arg(self.Y, X.dtype, (M, N), "Y", dev), _ptr(self.workspace),
-                      self.workspace.numel(), s)
+        self.Y, self.workspace, self._args = _run(
+            X.device, stream, lambda s: _linear_args(X, WC, WS, bias, Y, workspace, s))
 
     def __call__(self) -> torch.Tensor:
         code = self._fn(*self._args)
@@ -729,40 +745,45 @@ class Mxfp4LinearPlan:
 
 def _residual_norm(X, residual, weight, bias, norm, post_norm, post_weight, post_bias, gate, scale,
                    eps, H, Y, codes, scales, want_y, want_codes, stream):
-    px, ld = _rows(X, _DTYPES16, "X")
-    M, K = X.shape
+    M, K, px, ld = _rows(X, _DTYPES16, "X")
     dev, dt = X.device, X.dtype
     if norm not in NORMS or post_norm not in NORMS:
         raise ValueError(f"norm and post_norm are one of {', '.join(map(repr, NORMS))}")
-    pr, ldr = (None, K) if residual is None else _rows(residual, (dt,), "residual")
-    if residual is not None and (residual.shape != X.shape or residual.device != dev):
-        raise ValueError("residual must have X's shape and device")
-    G = 1
+    pr, ldr = None, K
+    if residual is not None:
+        if residual.shape != X.shape or residual.device != dev:
+            raise ValueError("residual must have X's shape and device")
+        _, _, pr, ldr = _rows(residual, (dt,), "residual")
+    G, pg = 1, None
     if gate is not None:
-        G = gate.shape[0] if gate.dim() == 2 else 1
         if gate.dim() == 1:
             gate = gate.view(1, -1)
+        G = gate.shape[0]
         if G < 1 or M % G:
             raise ValueError(f"the gate's {G} rows must divide X's {M}")
-    vec = lambda t, name: _arg(t, dt, (K,), name, dev)  # noqa: E731
-    shape = mxfp4_scales_shape(M, K)
-    with _running_on(dev, stream) as s:
-        H = torch.empty((M, K), dtype=dt, device=dev) if H is None else H
-        if want_y:
-            Y = torch.empty((M, K), dtype=dt, device=dev) if Y is None else Y
-        if want_codes:
-            codes = torch.empty((M, K // 2), dtype=torch.uint8, device=dev) if codes is None \
-                else codes
-            scales = torch.empty(shape, dtype=torch.uint8, device=dev) if scales is None \
-                else scales
+        pg = _arg(gate, dt, (G, K), "gate", dev)
+    vec = (K,)
+    pw, pb = _arg(weight, dt, vec, "weight", dev), _arg(bias, dt, vec, "bias", dev)
+    ppw = _arg(post_weight, dt, vec, "post_weight", dev)
+    ppb = _arg(post_bias, dt, vec, "post_bias", dev)
+    c_shape, s_shape = (M, K // 2), mxfp4_scales_shape(M, K)
+
+    def call(s):
+        h = X.new_empty((M, K)) if H is None else H
+        y, c, t = Y, codes, scales
+        if want_y and y is None:
+            y = X.new_empty((M, K))
+        if want_codes and c is None:
+            c = X.new_empty(c_shape, dtype=torch.uint8)
+        if want_codes and t is None:
+            t = X.new_empty(s_shape, dtype=torch.uint8)
         _check(load().llmint8_residual_norm(
-            px, DTYPES[dt], M, K, ld, pr, ldr, NORMS[post_norm], vec(post_weight, "post_weight"),
-            vec(post_bias, "post_bias"), _arg(gate, dt, (G, K), "gate", dev), G,
-            ctypes.c_float(scale), NORMS[norm], vec(weight, "weight"), vec(bias, "bias"),
-            ctypes.c_float(eps), _arg(H, dt, (M, K), "H", dev), _arg(Y, dt, (M, K), "Y", dev),
-            _arg(codes, torch.uint8, (M, K // 2), "codes", dev),
-            _arg(scales, torch.uint8, shape, "scales", dev), s), "llmint8_residual_norm")
-    return H, Y, codes, scales
+            px, DTYPES[dt], M, K, ld, pr, ldr, NORMS[post_norm], ppw, ppb, pg, G, scale,
+            NORMS[norm], pw, pb, eps, _arg(h, dt, (M, K), "H", dev), _arg(y, dt, (M, K), "Y", dev),
+            _arg(c, torch.uint8, c_shape, "codes", dev),
+            _arg(t, torch.uint8, s_shape, "scales", dev), s), "llmint8_residual_norm")
+        return h, y, c, t
+    return _run(dev, stream, call)
 
 
 def llmint8_residual_norm(X: torch.Tensor, residual=None, weight=None, bias=None,
