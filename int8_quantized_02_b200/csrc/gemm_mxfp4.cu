@@ -205,7 +205,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer ----
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t keep = l2_policy_evict_last();
             int stage = 0;
             uint32_t phase = 0, issued = 0;      // k-tiles whose loads are on their way
@@ -260,7 +260,10 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         }
     } else if (warp == 1) {
         // --------------------------------------------------------------- MMA issuer ----
-        if (lane == 0 && leader) {
+        if (!leader) {
+            // the second CTA's TMEM and shared memory are the leader's MMA operands until then
+            if (lane == 0) drain_wait(smem_addr(&tail->mma_done), 0, a.status);
+        } else if (elect_one()) {
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             int acc = 0, done = 0;
@@ -298,9 +301,6 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             }
             // every MMA issued by this thread has completed once mma_done arrives
             tc_commit_pair_both(smem_addr(&tail->mma_done));
-            drain_wait(smem_addr(&tail->mma_done), 0, a.status);
-        } else if (lane == 0) {
-            // the second CTA's TMEM and shared memory are the leader's MMA operands until then
             drain_wait(smem_addr(&tail->mma_done), 0, a.status);
         }
     } else {
@@ -546,7 +546,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     };
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             // Right behind the quantisation of X in one call, the weight does not depend on the
             // kernel that is still running: its first stages are on their way meanwhile.
             const int pre = a.weights_ready ? min(C::STAGES, k_count) : 0;
@@ -569,7 +569,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         }
     } else {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (warp == 1 && lane == 0) {
+        if (warp == 1 && elect_one()) {
             for (int it = 0; it < k_count; ++it) {
                 const int stage = it % C::STAGES;
                 if (!wait(smem_addr(&tail->full[stage]), (uint32_t)(it / C::STAGES) & 1u)) break;
