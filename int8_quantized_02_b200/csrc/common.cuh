@@ -369,9 +369,11 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
 // CTAs streaming different tiles at the same moment read different column ranges of the
 // 2^n-strided weight rows (spreading the requests over the DRAM channels) instead of all
 // hitting the same offset.  Integer accumulation makes the order irrelevant to the result.
+__host__ __device__ __forceinline__ int first_kblock(int tile, int kblocks) {
+    return (int)(((unsigned)tile * 7u) % (unsigned)kblocks);
+}
 __host__ __device__ __forceinline__ int rotated_kblock(int it, int tile, int kblocks) {
-    const int r = (int)(((unsigned)tile * 7u) % (unsigned)kblocks);
-    const int kb = it + r;
+    const int kb = it + first_kblock(tile, kblocks);
     return kb >= kblocks ? kb - kblocks : kb;
 }
 
@@ -421,6 +423,16 @@ __device__ __forceinline__ void tc_commit_pair_both(uint32_t bar) {
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                 map_to_rank(bar, r))
             : "memory");
+}
+// The same with one multicast commit.  Two commits a stage delay the next stage's MMAs by 60
+// clocks once their issuer waits on barriers in between; one does not (512 clocks for 512 clocks
+// of MMAs).
+__device__ __forceinline__ void tc_commit_pair_multicast(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),

@@ -212,6 +212,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             for (int tile = unit; tile < total; tile += units) {
                 const int mt = (tile % a.tiles_m) * 2 + (int)rank;   // this CTA's 128 rows of X
                 const int nt = (tile / a.tiles_m) * 2;               // the tile's 256 of W
+                int kr = first_kblock(tile / a.tiles_m, a.tiles_k);
                 for (int kb = 0; kb < a.tiles_k; ++kb) {
                     if (!wait(smem_addr(&tail->empty[stage]), phase ^ 1)) goto drain;
                     const uint32_t full = smem_addr(&tail->full[stage]);
@@ -219,7 +220,6 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     // the leader's barrier counts the bytes of both CTAs
                     if (leader) mbar_arrive_expect_tx(full, 2 * P_STAGE);
                     const uint32_t fbar = map_to_rank(full, 0);
-                    const int kr = rotated_kblock(kb, tile / a.tiles_m, a.tiles_k);
                     tma_load_2d_pair_hint(sa, &tmX, kr * KB, mt * ROWS, fbar, keep);
                     tma_load_2d_pair(sa + ROWS * KB, &tmW, kr * KB, (nt + (int)rank) * ROWS, fbar);
                     // scale tiles past the last row of tiles read as zero
@@ -228,6 +228,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     tma_load_2d_pair(ss + kMxTile, &tmWS, 0, nt * a.tiles_k + kr, fbar);
                     tma_load_2d_pair(ss + 2 * kMxTile, &tmWS, 0, (nt + 1) * a.tiles_k + kr, fbar);
                     ++issued;
+                    if (++kr == a.tiles_k) kr = 0;
                     if (++stage == P_STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -275,6 +276,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(acc * P_SHIFT);
                 bool ok = true;
+                int kr = first_kblock(tile / a.tiles_m, a.tiles_k);
                 for (int kb = 0; kb < a.tiles_k; ++kb) {
                     if (!wait(smem_addr(&tail->full[stage]), phase)) {
                         ok = false;
@@ -282,25 +284,25 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     }
                     tc_fence_after();
                     const uint32_t sa = smem_addr(smem + stage * P_STAGE);
-                    const int kr = rotated_kblock(kb, tile / a.tiles_m, a.tiles_k);
                     mma_ktile<true, 2 * ROWS, BN>(
                         d, sa, sa + ROWS * KB, sa + 2 * ROWS * KB, sa + 2 * ROWS * KB + kMxTile,
                         tmem + P_SF, kr == a.tiles_k - 1 ? a.last_mma : 4, kb == 0);
-                    tc_commit_pair_both(smem_addr(&tail->empty[stage]));
+                    tc_commit_pair_multicast(smem_addr(&tail->empty[stage]));
+                    if (++kr == a.tiles_k) kr = 0;
                     if (++stage == P_STAGES) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                tc_commit_pair_both(smem_addr(&tail->acc_full[acc]));
+                tc_commit_pair_multicast(smem_addr(&tail->acc_full[acc]));
                 if (++acc == 2) {
                     acc = 0;
                     acc_phase ^= 1;
                 }
             }
             // every MMA issued by this thread has completed once mma_done arrives
-            tc_commit_pair_both(smem_addr(&tail->mma_done));
+            tc_commit_pair_multicast(smem_addr(&tail->mma_done));
             drain_wait(smem_addr(&tail->mma_done), 0, a.status);
         }
     } else {
