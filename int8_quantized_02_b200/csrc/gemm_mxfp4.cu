@@ -109,8 +109,12 @@ constexpr int P_STAGES = 6;
 constexpr int P_STAGE = 2 * ROWS * KB + 3 * kMxTile;   // X, half of W, scales of X and of W
 constexpr int P_SHIFT = 224;             // first column of the second accumulator
 constexpr int P_SF = 480;                // first column of the scales
-constexpr int P_PITCH = 9;               // words of a staged row of 16 outputs, and one of padding
-constexpr int P_STAGING = EPI_WARPS * 32 * P_PITCH * 4;
+// Staging of a warp's 32 x 32 outputs: for a TMA store 64 bytes a row with the 64-byte swizzle, or
+// for rows of any alignment 16 outputs a row with a word of padding.
+constexpr int P_STAGE_OUT = 32 * 64;
+constexpr int P_PITCH = 9;
+constexpr int P_STAGING = EPI_WARPS * P_STAGE_OUT;
+static_assert(32 * P_PITCH * 4 <= P_STAGE_OUT, "staging");
 static_assert(P_SHIFT + BN <= P_SF && P_SF + 2 * 12 <= 512, "TMEM columns");
 
 struct PairTail {
@@ -127,7 +131,7 @@ struct PairTail {
     uint32_t peer_issued;
     int abort_flag;
 };
-constexpr int P_SMEM = P_STAGES * P_STAGE + P_STAGING + 1024 + (int)sizeof(PairTail);
+constexpr int P_SMEM = P_STAGES * P_STAGE + P_STAGING + (int)sizeof(PairTail);
 static_assert(P_SMEM <= 232448, "fits the opt-in shared memory of one CTA");
 
 struct PArgs {
@@ -156,11 +160,9 @@ template <int DT>
 __global__ void __launch_bounds__(P_THREADS, 1)
 mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                   const __grid_constant__ CUtensorMap tmXS, const __grid_constant__ CUtensorMap tmWS,
-                  const PArgs a) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint32_t *staging = reinterpret_cast<uint32_t *>(smem + P_STAGES * P_STAGE);
+                  const __grid_constant__ CUtensorMap tmY, const PArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *staging = smem + P_STAGES * P_STAGE;
     PairTail *tail = reinterpret_cast<PairTail *>(smem + P_STAGES * P_STAGE + P_STAGING);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -200,6 +202,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = tail->tmem_base;
     const BoundedWait wait{&tail->abort_flag, a.status, a.timeout_ns};
+    LLMINT8_DCHECK((smem_addr(smem) & 1023u) == 0, a.status);
     const int total = a.tiles_m * a.tiles_n;
     if (blockIdx.x == 0 && threadIdx.x == 0) a.status.set(LLMINT8_OK);
 
@@ -310,14 +313,13 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         const int q = warp & 3;                        // TMEM lane quadrant of this warp
         const int half = (warp - 2) / 4;               // its half of the tile's columns
         const uint32_t tl = tmem + ((uint32_t)(q * 32) << 16);
-        uint32_t *stg = staging + (warp - 2) * 32 * P_PITCH;
+        uint8_t *stg = staging + (warp - 2) * P_STAGE_OUT;
         const bool vec = (a.N & 7) == 0;               // rows of Y start on 16 bytes
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int tile = unit; tile < total; tile += units) {
             const int m0 = (tile % a.tiles_m) * 2 * ROWS + (int)rank * ROWS + q * 32;
             const int n0 = (tile / a.tiles_m) * BN;
-            const int row = m0 + lane;
             int ok = 0;
             if (lane == 0) ok = wait(smem_addr(&tail->acc_full[acc]), acc_phase) ? 1 : 0;
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -373,15 +375,18 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 for (int j = 0; j < 16; ++j)
                     p[j] = pack_pair<DT>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
                 if (vec) {
-                    if (row < a.M) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(
-                            static_cast<uint16_t *>(a.Y) + (int64_t)row * a.N + nb);
+                    // the warp's last store has read the staging
+                    if (lane == 0) bulk_wait_read();
+                    __syncwarp();
 #pragma unroll
-                        for (int g = 0; g < 4; ++g)
-                            if (nb + 8 * g < a.N)
-                                dst[g] = make_uint4(p[4 * g], p[4 * g + 1], p[4 * g + 2],
-                                                    p[4 * g + 3]);
-                    }
+                    for (int g = 0; g < 4; ++g)
+                        *reinterpret_cast<uint4 *>(stg + lane * 64 +
+                                                   ((g ^ ((lane >> 1) & 3)) << 4)) =
+                            make_uint4(p[4 * g], p[4 * g + 1], p[4 * g + 2], p[4 * g + 3]);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    // what lies past M or N is left out by the tensor map
+                    if (lane == 0 && m0 < a.M) tma_store_2d(&tmY, smem_addr(stg), nb, m0);
                 } else {
                     // rows of any alignment: turn 32 rows x 16 columns in shared memory, so that
                     // half a warp writes 16 neighbouring values of a row
@@ -389,7 +394,8 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     for (int g = 0; g < 2; ++g) {
                         __syncwarp();
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) stg[lane * P_PITCH + j] = p[g * 8 + j];
+                        for (int j = 0; j < 8; ++j)
+                            reinterpret_cast<uint32_t *>(stg)[lane * P_PITCH + j] = p[g * 8 + j];
                         __syncwarp();
                         const int n = nb + g * 16 + (lane & 15);
 #pragma unroll 4
@@ -398,7 +404,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                             if (n < a.N && m0 + rr < a.M)
                                 static_cast<uint16_t *>(a.Y)[(int64_t)(m0 + rr) * a.N + n] =
                                     reinterpret_cast<const uint16_t *>(
-                                        stg + rr * P_PITCH)[lane & 15];
+                                        stg + rr * P_PITCH * 4)[lane & 15];
                         }
                     }
                 }
@@ -414,6 +420,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 acc_phase ^= 1;
             }
         }
+        if (lane == 0) bulk_wait_all();
     }
 
     tc_fence_before();
@@ -464,7 +471,7 @@ struct BandTail {
 };
 template <int NT>
 constexpr int band_smem() {
-    return Band<NT>::STAGES * Band<NT>::STAGE + 1024 + (int)sizeof(BandTail);
+    return Band<NT>::STAGES * Band<NT>::STAGE + (int)sizeof(BandTail);
 }
 
 struct BArgs {
@@ -494,9 +501,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                   const BArgs a) {
     using C = Band<NT>;
     static_assert(C::STAGES <= kBandMaxStages, "barriers");
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
     BandTail *tail = reinterpret_cast<BandTail *>(smem + C::STAGES * C::STAGE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = a.splits;
@@ -526,6 +531,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = tail->tmem_base;
     const BoundedWait wait{&tail->abort_flag, a.status, a.timeout_ns};
+    LLMINT8_DCHECK((smem_addr(smem) & 1023u) == 0, a.status);
 
     auto load_w = [&](int it, int stage) {
         const uint32_t full = smem_addr(&tail->full[stage]);
@@ -779,6 +785,12 @@ cudaError_t gemm(const Mxfp4Gemm &g, cudaStream_t s) {
     }
     Maps t;
     if (!make_maps(&t, g, ROWS)) return cudaErrorInvalidValue;
+    // rows of Y on 16 bytes are stored by TMA
+    CUtensorMap tmY;
+    memset(&tmY, 0, sizeof(tmY));
+    if (g.N % 8 == 0 && !make_map(&tmY, g.Y, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, g.N, g.M, g.N, 32,
+                                  32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
     PArgs a;
     a.bias = g.bias;
     a.Y = g.Y;
@@ -793,7 +805,7 @@ cudaError_t gemm(const Mxfp4Gemm &g, cudaStream_t s) {
     const int pairs = std::min(a.tiles_m * a.tiles_n, sms / 2);
     auto k = g.dtype == kF16 ? mxfp4_pair_kernel<kF16> : mxfp4_pair_kernel<kBF16>;
     return launch_cluster(k, dim3((unsigned)(2 * pairs)), P_THREADS, P_SMEM, 2, s, t.X, t.W, t.XS,
-                          t.WS, a);
+                          t.WS, tmY, a);
 }
 
 }  // namespace
