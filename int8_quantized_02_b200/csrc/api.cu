@@ -750,7 +750,7 @@ llmint8_status llmint8_mxfp4_quantize(const void *X, int dtype, int64_t R, int64
     if (!X || !aligned16(X) || !mx_pair_ok(codes, scales) ||
         !pitch_ok(ldx, K, dtype == LLMINT8_F32 ? 4 : 2))
         return LLMINT8_ERR_INVALID_ARG;
-    return from_cuda(launch_mxfp4_quantize(X, dtype, ldx, R, align_up(R, 128), K, codes, scales,
+    return from_cuda(launch_mxfp4_quantize(X, dtype, ldx, R, true, K, codes, scales,
                                            static_cast<cudaStream_t>(stream)));
 }
 
@@ -781,7 +781,7 @@ llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t
     uint8_t *Xc = at<uint8_t>(ws, L.codes), *Xs = at<uint8_t>(ws, L.scales);
     // rows past M of the last scale tile meet only codes that read as zero, in columns of the
     // product that are not stored: they stay as they are
-    if (launch_mxfp4_quantize(X, dtype, ldx, M, M, K, Xc, Xs, s) != cudaSuccess)
+    if (launch_mxfp4_quantize(X, dtype, ldx, M, false, K, Xc, Xs, s) != cudaSuccess)
         return LLMINT8_ERR_CUDA;
     return run_mxfp4(Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 1, ws, s);
 }

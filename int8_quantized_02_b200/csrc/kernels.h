@@ -149,11 +149,10 @@ cudaError_t launch_decode(const DecodeLaunch &d, cudaStream_t s);
 namespace llmint8 {
 
 // MXFP4 (mxfp4.cu): codes uint8 [R, K/2], scales uint8 [ceil(R/128)][ceil(K/256)][1024].  dtype is
-// a llmint8_dtype.  rows_out >= R: scales of rows [R, rows_out) are written as zero (R, or R
-// rounded up to 128 where the whole buffer is to be defined).
-cudaError_t launch_mxfp4_quantize(const void *X, int dtype, int64_t ldx, int64_t R,
-                                  int64_t rows_out, int64_t K, uint8_t *codes, uint8_t *scales,
-                                  cudaStream_t s);
+// a llmint8_dtype.  pad: the scales of every row up to a multiple of 128 are written (zero past R);
+// without it some stay as they are.
+cudaError_t launch_mxfp4_quantize(const void *X, int dtype, int64_t ldx, int64_t R, bool pad,
+                                  int64_t K, uint8_t *codes, uint8_t *scales, cudaStream_t s);
 cudaError_t launch_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t R,
                                  int64_t K, void *out, int dtype, cudaStream_t s);
 

@@ -1,10 +1,11 @@
 // MXFP4 quantisation of the rows of a matrix, and the way back.  Both are bound by HBM: they
 // read and write each value once (17/32 byte an element in MXFP4 form) and compute little.
 //
-// A warp takes one row of a scale tile (256 columns, 8 elements a lane), so a block's maximum is
-// two shuffles among four lanes, its codes one 32-bit store a lane and the row's eight scales two
-// 32-bit stores.  A warp keeps U such pieces in flight (U = 4 once the grid fills the machine
-// several times over; 1 below that, where more warps hide more latency than deeper ones).
+// A warp takes 256 columns (a scale tile's width, 8 elements a lane) of the four rows r, r + 32,
+// r + 64 and r + 96 of a scale tile, all of whose loads are in flight at once.  A block's maximum
+// is two shuffles among four lanes, its codes one 32-bit store a lane; and the scales of those
+// four rows are neighbours in the tile, so that half a warp's four blocks of each row make one
+// 16-byte store.  (With one row to a warp and 4-byte stores: 38 us for [16384, 4096] fp16.)
 #include "kernels.h"
 #include "launch.cuh"
 #include "mxfp4.cuh"
@@ -16,72 +17,72 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// The pieces of a warp: row `row`, scale-tile columns kt0 + i * step (i < U).
+constexpr int kRows = 4;                 // rows of a warp, 32 apart
+
+// A warp's tile column and first row.
 struct Place {
-    int64_t row;
-    int64_t kt0;
-    int step;
+    int64_t row, kt;
 };
-template <int U>
 __device__ __forceinline__ Place place_of_warp(int wpr_log2) {
     const int w = threadIdx.x >> 5;
-    Place p;
-    p.step = 1 << wpr_log2;
-    p.row = (int64_t)blockIdx.x * (kWarps >> wpr_log2) + (w >> wpr_log2);
-    p.kt0 = (int64_t)blockIdx.y * (U << wpr_log2) + (w & (p.step - 1));
-    return p;
+    const int64_t g = (int64_t)blockIdx.x * (kWarps >> wpr_log2) + (w >> wpr_log2);
+    return Place{(g >> 5) * kMxRows + (g & 31),
+                 ((int64_t)blockIdx.y << wpr_log2) + (w & ((1 << wpr_log2) - 1))};
 }
 
-// rows_out >= R: rows [R, rows_out) get zero scales (they pad the last row of scale tiles).
-template <int DT, int U>
+// Rows R to the next multiple of 128 get zero scales; with `pad` false that is left out for those
+// that no row below R shares a store with.
+template <int DT>
 __global__ void __launch_bounds__(kThreads)
-mxfp4_quantize_kernel(const uint8_t *__restrict__ X, int64_t row_bytes, int64_t R,
-                      int64_t rows_out, int64_t chunks, int64_t tiles_k, int wpr_log2,
+mxfp4_quantize_kernel(const uint8_t *__restrict__ X, int64_t row_bytes, int64_t R, bool pad,
+                      int64_t chunks, int64_t tiles_k, int wpr_log2,
                       uint32_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31;
-    const Place p = place_of_warp<U>(wpr_log2);
-    if (p.row >= rows_out) return;
-    Chunk<DT> c[U];
+    const Place p = place_of_warp(wpr_log2);
+    if (p.kt >= tiles_k || (!pad && p.row >= R)) return;
+    const int64_t ch = p.kt * 32 + lane;
+    const uint8_t *x = X + p.row * row_bytes;
+    Chunk<DT> c[kRows];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {        // issue every load before using any
-        const int64_t ch = (p.kt0 + i * p.step) * 32 + lane;
-        c[i] = p.row < R && ch < chunks ? load_chunk<DT>(X + p.row * row_bytes, ch)
-                                        : zero_chunk<DT>();
-    }
+    for (int j = 0; j < kRows; ++j)      // issue every load before using any
+        c[j] = p.row + 32 * j < R && ch < chunks ? load_chunk<DT>(x + 32 * j * row_bytes, ch)
+                                                 : zero_chunk<DT>();
+    uint32_t *q = codes + p.row * chunks + ch;
+    uint32_t word[kRows];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int64_t kt = p.kt0 + i * p.step;
-        if (kt < tiles_k)
-            quantize_tile_row<DT>(c[i], p.row < R && kt * 32 + lane < chunks, p.row, kt, chunks,
-                                  tiles_k, codes, scales, lane);
+    for (int j = 0; j < kRows; ++j) {
+        const uint32_t v = quantize_chunk<DT>(c[j], word[j], lane);
+        if (p.row + 32 * j < R && ch < chunks) q[32 * j * chunks] = v;
     }
+    if ((lane & 15) == 0)
+        *reinterpret_cast<uint4 *>(scales + scale_word_offset(p.row, p.kt, tiles_k, lane >> 4)) =
+            make_uint4(word[0], word[1], word[2], word[3]);
 }
 
-template <int DT, int U>
+template <int DT>
 __global__ void __launch_bounds__(kThreads)
 mxfp4_dequant_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restrict__ scales,
                      int64_t R, int64_t chunks, int64_t tiles_k, int wpr_log2,
                      uint8_t *__restrict__ out) {
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31;
-    const Place p = place_of_warp<U>(wpr_log2);
-    if (p.row >= R) return;
-    uint32_t q[U], s[U];
+    const Place p = place_of_warp(wpr_log2);
+    const int64_t ch = p.kt * 32 + lane;
+    if (ch >= chunks) return;
+    uint32_t q[kRows];
+    const uint32_t *at = codes + p.row * chunks + ch;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {        // issue every load before using any
-        const int64_t kt = p.kt0 + i * p.step;
-        q[i] = 0u;
-        s[i] = 0u;
-        if (kt * 32 + lane < chunks) {
-            q[i] = codes[p.row * chunks + kt * 32 + lane];
-            s[i] = scales[scale_word_offset(p.row, kt, tiles_k, lane >> 4) + ((lane >> 2) & 3)];
-        }
-    }
+    for (int j = 0; j < kRows; ++j)      // issue every load before using any
+        q[j] = p.row + 32 * j < R ? at[32 * j * chunks] : 0u;
+    const uint4 words = *reinterpret_cast<const uint4 *>(
+        scales + scale_word_offset(p.row, p.kt, tiles_k, lane >> 4));
+    const uint32_t word[kRows] = {words.x, words.y, words.z, words.w};
+    constexpr int kBytes = DT == kF32 ? 32 : 16;
+    uint8_t *o = out + p.row * chunks * kBytes;
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        const int64_t ch = (p.kt0 + i * p.step) * 32 + lane;
-        if (ch >= chunks) continue;
+    for (int j = 0; j < kRows; ++j) {
+        if (p.row + 32 * j >= R) break;
         uint32_t h[4];
         asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
             "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -90,11 +91,12 @@ mxfp4_dequant_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restri
             "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
             "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
             : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-            : "r"(q[i]));
+            : "r"(q[j]));
         // 2^(s - 127): an exponent field, or the subnormal 2^-127; 255 stands for NaN
-        const float scale = __uint_as_float(s[i] == 0u     ? 0x00400000u
-                                            : s[i] == 255u ? 0x7fc00000u
-                                                           : s[i] << 23);
+        const uint32_t s = (word[j] >> (8 * ((lane >> 2) & 3))) & 0xffu;
+        const float scale = __uint_as_float(s == 0u     ? 0x00400000u
+                                            : s == 255u ? 0x7fc00000u
+                                                        : s << 23);
         float f[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -102,80 +104,52 @@ mxfp4_dequant_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restri
             f[2 * e] = t.x * scale;      // exact but beyond fp32's range
             f[2 * e + 1] = t.y * scale;
         }
-        store_chunk<DT>(out + p.row * chunks * (DT == kF32 ? 32 : 16), ch, pack_chunk<DT>(f));
+        store_chunk<DT>(o + 32 * j * chunks * kBytes, ch, pack_chunk<DT>(f));
     }
 }
 
-// Warps to a row (1, 2, 4 or 8 of a CTA's 8), and the CTAs, for pieces of U scale tiles.
+// Warps to a row (1, 2, 4 or 8 of a CTA's 8), and the CTAs.
 struct Shape {
     int wpr_log2;
     dim3 grid;
 };
-Shape shape_for(int64_t rows, int64_t tiles_k, int U) {
+Shape shape_for(int64_t R, int64_t tiles_k) {
     Shape s;
     s.wpr_log2 = 0;
-    while (s.wpr_log2 < 3 && ((int64_t)U << s.wpr_log2) < tiles_k) ++s.wpr_log2;
-    s.grid = dim3((unsigned)ceil_div(rows, kWarps >> s.wpr_log2),
-                  (unsigned)ceil_div(tiles_k, (int64_t)U << s.wpr_log2));
+    while (s.wpr_log2 < 3 && (1 << s.wpr_log2) < tiles_k) ++s.wpr_log2;
+    const int64_t groups = ceil_div(R, kMxRows) * 32;
+    s.grid = dim3((unsigned)ceil_div(groups, kWarps >> s.wpr_log2),
+                  (unsigned)ceil_div(tiles_k, 1 << s.wpr_log2));
     return s;
-}
-// Four pieces a warp once that still leaves every SM (148, up to 64 warps each) full twice over.
-bool deep(int64_t rows, int64_t tiles_k) { return rows * tiles_k >= 4 * 2 * 148 * 64; }
-
-template <int DT, int U>
-cudaError_t quantize_launch(const void *X, int64_t row_bytes, int64_t R, int64_t rows_out,
-                            int64_t K, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
-    const int64_t tiles_k = ceil_div(K, kMxCols);
-    const Shape sh = shape_for(rows_out, tiles_k, U);
-    return launch_pdl(mxfp4_quantize_kernel<DT, U>, sh.grid, dim3(kThreads), s,
-                      static_cast<const uint8_t *>(X), row_bytes, R, rows_out, K / 8, tiles_k,
-                      sh.wpr_log2, reinterpret_cast<uint32_t *>(codes), scales);
-}
-
-template <int DT, int U>
-cudaError_t dequant_launch(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K,
-                           void *out, cudaStream_t s) {
-    const int64_t tiles_k = ceil_div(K, kMxCols);
-    const Shape sh = shape_for(R, tiles_k, U);
-    return launch_pdl(mxfp4_dequant_kernel<DT, U>, sh.grid, dim3(kThreads), s,
-                      reinterpret_cast<const uint32_t *>(codes), scales, R, K / 8, tiles_k,
-                      sh.wpr_log2, static_cast<uint8_t *>(out));
 }
 
 }  // namespace
 
-cudaError_t launch_mxfp4_quantize(const void *X, int dtype, int64_t ldx, int64_t R,
-                                  int64_t rows_out, int64_t K, uint8_t *codes, uint8_t *scales,
-                                  cudaStream_t s) {
-    const int64_t rb = ldx * (dtype == kF32 ? 4 : 2);
-    const bool d = deep(rows_out, ceil_div(K, kMxCols));
-    cudaError_t e;
-    if (dtype == kF16)
-        e = d ? quantize_launch<kF16, 4>(X, rb, R, rows_out, K, codes, scales, s)
-              : quantize_launch<kF16, 1>(X, rb, R, rows_out, K, codes, scales, s);
-    else if (dtype == kBF16)
-        e = d ? quantize_launch<kBF16, 4>(X, rb, R, rows_out, K, codes, scales, s)
-              : quantize_launch<kBF16, 1>(X, rb, R, rows_out, K, codes, scales, s);
-    else
-        e = d ? quantize_launch<kF32, 4>(X, rb, R, rows_out, K, codes, scales, s)
-              : quantize_launch<kF32, 1>(X, rb, R, rows_out, K, codes, scales, s);
+cudaError_t launch_mxfp4_quantize(const void *X, int dtype, int64_t ldx, int64_t R, bool pad,
+                                  int64_t K, uint8_t *codes, uint8_t *scales, cudaStream_t s) {
+    const int64_t tiles_k = ceil_div(K, kMxCols);
+    const Shape sh = shape_for(R, tiles_k);
+    auto k = dtype == kF16    ? mxfp4_quantize_kernel<kF16>
+             : dtype == kBF16 ? mxfp4_quantize_kernel<kBF16>
+                              : mxfp4_quantize_kernel<kF32>;
+    const cudaError_t e =
+        launch_pdl(k, sh.grid, dim3(kThreads), s, static_cast<const uint8_t *>(X),
+                   ldx * (dtype == kF32 ? 4 : 2), R, pad, K / 8, tiles_k, sh.wpr_log2,
+                   reinterpret_cast<uint32_t *>(codes), scales);
     note_launches(1);
     return e;
 }
 
 cudaError_t launch_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, int64_t R,
                                  int64_t K, void *out, int dtype, cudaStream_t s) {
-    const bool d = deep(R, ceil_div(K, kMxCols));
-    cudaError_t e;
-    if (dtype == kF16)
-        e = d ? dequant_launch<kF16, 4>(codes, scales, R, K, out, s)
-              : dequant_launch<kF16, 1>(codes, scales, R, K, out, s);
-    else if (dtype == kBF16)
-        e = d ? dequant_launch<kBF16, 4>(codes, scales, R, K, out, s)
-              : dequant_launch<kBF16, 1>(codes, scales, R, K, out, s);
-    else
-        e = d ? dequant_launch<kF32, 4>(codes, scales, R, K, out, s)
-              : dequant_launch<kF32, 1>(codes, scales, R, K, out, s);
+    const int64_t tiles_k = ceil_div(K, kMxCols);
+    const Shape sh = shape_for(R, tiles_k);
+    auto k = dtype == kF16    ? mxfp4_dequant_kernel<kF16>
+             : dtype == kBF16 ? mxfp4_dequant_kernel<kBF16>
+                              : mxfp4_dequant_kernel<kF32>;
+    const cudaError_t e = launch_pdl(k, sh.grid, dim3(kThreads), s,
+                                     reinterpret_cast<const uint32_t *>(codes), scales, R, K / 8,
+                                     tiles_k, sh.wpr_log2, static_cast<uint8_t *>(out));
     note_launches(1);
     return e;
 }

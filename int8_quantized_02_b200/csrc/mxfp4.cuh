@@ -168,28 +168,20 @@ __device__ __forceinline__ int64_t scale_word_offset(int64_t row, int64_t kt, in
     return ((row / kMxRows) * tiles_k + kt) * kMxTile + h * 512 + (r & 31) * 16 + (r >> 5) * 4;
 }
 
-// Warp-wide: quantises the 256 columns [256 kt, 256 kt + 256) of a row whose chunks the lanes
-// hold (zero past K), writes the codes of lanes with `store` and the row's eight scales.
+// Warp-wide: quantises 256 columns of a row whose chunks the lanes hold (zero past K).  Returns
+// this lane's eight codes; `word` gets the scale bytes of its half warp's four blocks.
 template <int DT>
-__device__ __forceinline__ void quantize_tile_row(const Chunk<DT> &c, bool store, int64_t row,
-                                                  int64_t kt, int64_t chunks, int64_t tiles_k,
-                                                  uint32_t *codes, uint8_t *scales, int lane) {
+__device__ __forceinline__ uint32_t quantize_chunk(const Chunk<DT> &c, uint32_t &word, int lane) {
     uint32_t m = chunk_absmax_bits<DT>(c);
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const uint32_t s = scale_byte<DT>(m);
-    if (store) {
-        float f[8];
-        unpack_chunk<DT>(c, f);
-        codes[row * chunks + kt * 32 + lane] = e2m1_codes(f, inverse_scale(s));
-    }
-    // the four scale bytes of each half warp, in one word
-    uint32_t word = s << (8 * ((lane >> 2) & 3));
+    word = s << (8 * ((lane >> 2) & 3));
     word |= __shfl_xor_sync(0xffffffffu, word, 4);
     word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if ((lane & 15) == 0)
-        *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, kt, tiles_k, lane >> 4)) =
-            word;
+    float f[8];
+    unpack_chunk<DT>(c, f);
+    return e2m1_codes(f, inverse_scale(s));
 }
 
 }  // namespace llmint8

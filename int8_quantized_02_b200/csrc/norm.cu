@@ -149,9 +149,15 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
             if (a.Y) store_chunk<DT>(static_cast<uint8_t *>(a.Y) + row * a.K * 2, ch, y);
         }
         // a warp's 32 chunks are one row's share of a scale tile; rows past M pad the last one
-        if (a.codes && row < a.rows_out && (ch >> 5) < a.tiles_k)
-            quantize_tile_row<DT>(y, in[i], row, ch >> 5, chunks, a.tiles_k,
-                                  reinterpret_cast<uint32_t *>(a.codes), a.scales, lane);
+        const int64_t kt = ch >> 5;
+        if (a.codes && row < a.rows_out && kt < a.tiles_k) {
+            uint32_t word;
+            const uint32_t q = quantize_chunk<DT>(y, word, lane);
+            if (in[i]) reinterpret_cast<uint32_t *>(a.codes)[row * chunks + ch] = q;
+            if ((lane & 15) == 0)
+                *reinterpret_cast<uint32_t *>(
+                    a.scales + scale_word_offset(row, kt, a.tiles_k, lane >> 4)) = word;
+        }
     }
 }
 
