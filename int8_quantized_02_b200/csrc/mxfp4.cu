@@ -104,7 +104,21 @@ mxfp4_dequant_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restri
             f[2 * e] = t.x * scale;      // exact but beyond fp32's range
             f[2 * e + 1] = t.y * scale;
         }
-        store_chunk<DT>(o + 32 * j * chunks * kBytes, ch, pack_chunk<DT>(f));
+        if constexpr (DT == kF32) {
+            // two neighbours trade halves, so that each store of the warp is one run of bytes
+            // (chunks come in fours, so both are there)
+            const bool odd = lane & 1;
+            float g[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                g[e] = __shfl_xor_sync(__activemask(), odd ? f[e] : f[4 + e], 1);
+            float4 *pair = reinterpret_cast<float4 *>(o + 32 * j * chunks * kBytes) + (ch & ~1) * 2 +
+                           (lane & 1);
+            pair[0] = odd ? make_float4(g[0], g[1], g[2], g[3]) : make_float4(f[0], f[1], f[2], f[3]);
+            pair[2] = odd ? make_float4(f[4], f[5], f[6], f[7]) : make_float4(g[0], g[1], g[2], g[3]);
+        } else {
+            store_chunk<DT>(o + 32 * j * chunks * kBytes, ch, pack_chunk<DT>(f));
+        }
     }
 }
 

@@ -42,6 +42,17 @@ __device__ __forceinline__ Chunk<DT> load_chunk(const void *base, int64_t chunk)
     return c;
 }
 
+// The same for what is read once: it leaves L1 to the vectors that every row reads.
+template <int DT>
+__device__ __forceinline__ Chunk<DT> stream_chunk(const void *base, int64_t chunk) {
+    static_assert(DT != kF32, "16-bit rows");
+    Chunk<DT> c;
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(c.w[0]), "=r"(c.w[1]), "=r"(c.w[2]), "=r"(c.w[3])
+                 : "l"(reinterpret_cast<const uint4 *>(base) + chunk));
+    return c;
+}
+
 template <int DT>
 __device__ __forceinline__ Chunk<DT> zero_chunk() {
     Chunk<DT> c;

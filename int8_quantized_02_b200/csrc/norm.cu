@@ -54,26 +54,38 @@ __device__ __forceinline__ void row_norm(const float (&v)[NCH][8], const bool (&
         mean = row_sum(s, red, tpr) * inv_k;
     }
     float q = 0.0f;
+    if (kind == LLMINT8_NORM_LAYER) {
 #pragma unroll
-    for (int i = 0; i < NCH; ++i)
-        if (in[i]) {
+        for (int i = 0; i < NCH; ++i)
+            if (in[i]) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) q = fmaf(v[i][e] - mean, v[i][e] - mean, q);
-        }
+                for (int e = 0; e < 8; ++e) q = fmaf(v[i][e] - mean, v[i][e] - mean, q);
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) q = fmaf(v[i][e], v[i][e], q);
+    }
     rstd = rsqrtf(row_sum(q, red + kMaxWarps, tpr) * inv_k + eps);
 }
 
 // v = (v - mean) * rstd * w + b over one chunk; w and b may be null.
 template <int DT>
-__device__ __forceinline__ void apply_norm(float (&v)[8], float mean, float rstd, const void *w,
-                                           const void *b, int64_t ch) {
+__device__ __forceinline__ void apply_norm(float (&v)[8], int kind, float mean, float rstd,
+                                           const void *w, const void *b, int64_t ch) {
+    if (kind == LLMINT8_NORM_LAYER) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = (v[e] - mean) * rstd;
+        for (int e = 0; e < 8; ++e) v[e] -= mean;
+    }
     float t[8];
     if (w) {
         unpack_chunk<DT>(load_chunk<DT>(w, ch), t);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= t[e];
+        for (int e = 0; e < 8; ++e) v[e] *= rstd * t[e];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] *= rstd;
     }
     if (b) {
         unpack_chunk<DT>(load_chunk<DT>(b, ch), t);
@@ -82,8 +94,8 @@ __device__ __forceinline__ void apply_norm(float (&v)[8], float mean, float rstd
     }
 }
 
-template <int DT, int NCH>
-__global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a, int tpr_log2) {
+template <int DT, int NCH, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) residual_norm_kernel(const NormArgs a, int tpr_log2) {
     pdl_wait_then_release();
     __shared__ float red[4 * kMaxWarps];
     const int tpr = 1 << tpr_log2;
@@ -103,8 +115,8 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
     for (int i = 0; i < NCH; ++i) {      // issue every load before using any
         const int64_t ch = t + ((int64_t)i << tpr_log2);
         in[i] = live && ch < chunks;
-        x[i] = in[i] ? load_chunk<DT>(xr, ch) : zero_chunk<DT>();
-        r[i] = in[i] && rr ? load_chunk<DT>(rr, ch) : zero_chunk<DT>();
+        x[i] = in[i] ? stream_chunk<DT>(xr, ch) : zero_chunk<DT>();
+        r[i] = in[i] && rr ? stream_chunk<DT>(rr, ch) : zero_chunk<DT>();
     }
     float h[NCH][8];
 #pragma unroll
@@ -115,7 +127,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
             if (in[i])
-                apply_norm<DT>(h[i], mean, rstd, a.post_weight, a.post_bias,
+                apply_norm<DT>(h[i], a.post_norm, mean, rstd, a.post_weight, a.post_bias,
                                t + ((int64_t)i << tpr_log2));
     }
     const uint8_t *gr = a.gate ? static_cast<const uint8_t *>(a.gate) +
@@ -144,7 +156,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
         const int64_t ch = t + ((int64_t)i << tpr_log2);
         Chunk<DT> y = zero_chunk<DT>();
         if (in[i]) {
-            apply_norm<DT>(h[i], mean, rstd, a.weight, a.bias, ch);
+            apply_norm<DT>(h[i], a.norm, mean, rstd, a.weight, a.bias, ch);
             y = pack_chunk<DT>(h[i]);
             if (a.Y) store_chunk<DT>(static_cast<uint8_t *>(a.Y) + row * a.K * 2, ch, y);
         }
@@ -163,19 +175,45 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
 
 template <int DT>
 cudaError_t norm_launch(const NormArgs &a, cudaStream_t s) {
-    // Threads to a row: enough for at most 4 chunks each; while the grid is small, one chunk each,
-    // since a lone row's time is its chain of latencies.
+    // Threads to a row (a power of two) and chunks to a thread (at most 4): what leaves the fewest
+    // idle; of equals, up to 256 threads and then two chunks, since several rows to an SM, in
+    // CTAs of their own, keep its memory busy while one of them waits for its sums.  A few rows
+    // take one chunk a thread: a lone row's time is its chain of latencies.
     const int64_t chunks = ceil_div(a.K, kMxCols) * 32;
-    const int want = a.M <= 148 ? 1 : 2;
-    int tpr_log2 = 5;
-    while (tpr_log2 < 10 && ((int64_t)want << tpr_log2) < chunks) ++tpr_log2;
-    const int64_t per = ceil_div(chunks, (int64_t)1 << tpr_log2);
-    const int threads = std::max(1 << tpr_log2, 128);
+    int best = 10;
+    if (a.M <= 148) {
+        best = 5;
+        while (best < 10 && ((int64_t)1 << best) < chunks) ++best;
+    } else {
+        int64_t least = INT64_MAX;
+        for (int l = 5; l <= 10; ++l) {
+            const int64_t n = ceil_div(chunks, (int64_t)1 << l);
+            if (n > 4) continue;
+            const int64_t cost = ((n << l) << 4) + (l > 8 ? 4 : 0) + (n == 1 ? 2 : 0) + n;
+            if (cost < least) {
+                least = cost;
+                best = l;
+            }
+        }
+    }
+    const int per = (int)ceil_div(chunks, (int64_t)1 << best);
+    const int threads = std::max(1 << best, 256);
     const int64_t rows = a.codes ? a.rows_out : a.M;
-    const dim3 grid((unsigned)ceil_div(rows, threads >> tpr_log2));
-    if (per <= 1) return launch_pdl(residual_norm_kernel<DT, 1>, grid, dim3(threads), s, a, tpr_log2);
-    if (per <= 2) return launch_pdl(residual_norm_kernel<DT, 2>, grid, dim3(threads), s, a, tpr_log2);
-    return launch_pdl(residual_norm_kernel<DT, 4>, grid, dim3(threads), s, a, tpr_log2);
+    const dim3 grid((unsigned)ceil_div(rows, threads >> best));
+    const auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(threads), s, a, best); };
+    if (threads == 256) {
+        if (per == 1) return go(residual_norm_kernel<DT, 1, 256, 8>);
+        if (per == 2) return go(residual_norm_kernel<DT, 2, 256, 6>);
+        return per == 3 ? go(residual_norm_kernel<DT, 3, 256, 4>)
+                        : go(residual_norm_kernel<DT, 4, 256, 4>);
+    }
+    if (threads == 512)
+        return per == 1 ? go(residual_norm_kernel<DT, 1, 512, 2>)
+                        : per <= 3 ? go(residual_norm_kernel<DT, 3, 512, 2>)
+                                   : go(residual_norm_kernel<DT, 4, 512, 2>);
+    return per == 1 ? go(residual_norm_kernel<DT, 1, 1024, 1>)
+                    : per == 2 ? go(residual_norm_kernel<DT, 2, 1024, 1>)
+                               : go(residual_norm_kernel<DT, 4, 1024, 1>);
 }
 
 }  // namespace
