@@ -396,8 +396,8 @@ LLMINT8_API llmint8_status llmint8_mxfp4_dequant(const uint8_t *codes, const uin
  *   ws      device workspace of llmint8_mxfp4_linear_workspace_size(M, N, K) bytes; its device
  *           status is read with llmint8_device_status().  Calls that may overlap need a workspace
  *           each; calls in stream order may share one.
- * Kernels: at most 256 rows of X stream the weight as the MMA's 128-row operand, k split over the
- * CTAs of a cluster; more run CTA pairs on 256 x 256 tiles.  Results do not depend on timing; the
+ * Kernels: few rows of X stream the weight as the MMA's 128-row operand, k split over the CTAs of
+ * a cluster; more run CTA pairs on 256 x 256 tiles.  Results do not depend on timing; the
  * same rows in calls of different M may differ in the last fp32 rounding of a sum.
  */
 LLMINT8_API llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t K,

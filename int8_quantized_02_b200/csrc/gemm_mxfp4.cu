@@ -16,7 +16,7 @@
 //         of the weight rows each), persistent, 6 stages.  Two 256-column accumulators and 24
 //         columns of scales do not fit TMEM's 512, so the two accumulators overlap by 32 columns:
 //         the epilogue takes those first, and the next tile's MMAs wait for them alone.
-//   band  few rows of X: the weight is the MMA's 128-row operand and up to 256 rows of X its
+//   band  few rows of X: the weight is the MMA's 128-row operand and up to 64 rows of X its
 //         columns, so each weight byte enters one SM once.  The k range of a band of 128 weight
 //         rows is split over the S CTAs of a cluster, which add their partial sums through
 //         distributed shared memory in rank order (the result does not depend on timing).
@@ -80,10 +80,12 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
 }
 
 // The MMAs of one k-tile.  `n_mma` (1 to 4) leaves out 64-column steps past K.
-// TMEM at `sf`: for each pair of steps 4 columns of A's scales, then 4 for each 128 rows of B.
+// TMEM at `sf`: for each pair of steps 4 columns of A's scales, then 4 for each 128 rows of B, of
+// which B's rows begin at column `b0` (a column holds 32 rows).
 template <bool PAIR, int M, int N>
 __device__ __forceinline__ void mma_ktile(uint32_t d, uint32_t sa, uint32_t sb, uint32_t ssfa,
-                                          uint32_t ssfb, uint32_t sf, int n_mma, bool first) {
+                                          uint32_t ssfb, uint32_t sf, uint32_t b0, int n_mma,
+                                          bool first) {
     constexpr int NB = (N + 127) / 128;
     constexpr uint32_t kCols = 4 + 4 * NB;
 #pragma unroll
@@ -97,7 +99,7 @@ __device__ __forceinline__ void mma_ktile(uint32_t d, uint32_t sa, uint32_t sb, 
         for (int k = 2 * h; k < 2 * h + 2; ++k)
             if (k < n_mma)
                 mma_mxf4<PAIR>(d, sw128_desc(sa + 32 * k), sw128_desc(sb + 32 * k),
-                               idesc_mxf4(M, N, 2 * (k & 1)), t, t + 4, !first || k != 0);
+                               idesc_mxf4(M, N, 2 * (k & 1)), t, t + 4 + b0, !first || k != 0);
     }
 }
 
@@ -289,7 +291,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     const uint32_t sa = smem_addr(smem + stage * P_STAGE);
                     mma_ktile<true, 2 * ROWS, BN>(
                         d, sa, sa + ROWS * KB, sa + 2 * ROWS * KB, sa + 2 * ROWS * KB + kMxTile,
-                        tmem + P_SF, kr == a.tiles_k - 1 ? a.last_mma : 4, kb == 0);
+                        tmem + P_SF, 0, kr == a.tiles_k - 1 ? a.last_mma : 4, kb == 0);
                     tc_commit_pair_multicast(smem_addr(&tail->empty[stage]));
                     if (++kr == a.tiles_k) kr = 0;
                     if (++stage == P_STAGES) {
@@ -448,19 +450,22 @@ template <int NT>
 struct Band {
     static constexpr int NB = (NT + 127) / 128;        // scale tiles of X
     static constexpr int STAGE = ROWS * KB + NT * KB + (1 + NB) * kMxTile;
-    // about 100 KB, so that two CTAs share an SM; 256 rows of X take the whole of it
-    static constexpr int STAGES = NT == 256 ? 4 : 104 * 1024 / STAGE;
+    // Stages of a CTA that has an SM, or half of one, to itself: about 100 KB, so that two fit; and
+    // where the grid fills the machine more than twice, about 60 KB, so that a third CTA covers the
+    // others' first loads and last stores (8 x 49152 x 12288: 53.7 us with 5 stages, 50.2 with 3).
+    // TMEM never runs out: the CTAs that fit an SM's shared memory hold 512 columns at most.
+    static constexpr int STAGES = 104 * 1024 / STAGE;
+    static constexpr int FEW = NT == 64 ? 2 : 3;
     static constexpr uint32_t SF = NT;                 // TMEM: accumulator, then the scales
     static constexpr uint32_t COLS_USED = NT + 2 * (4 + 4 * NB);
     static constexpr uint32_t COLS = COLS_USED <= 32    ? 32
                                      : COLS_USED <= 64  ? 64
-                                     : COLS_USED <= 128 ? 128
-                                     : COLS_USED <= 256 ? 256
-                                                        : 512;
+                                                        : 128;
+    static_assert(COLS_USED <= COLS, "TMEM columns");
     static_assert(STAGE % 1024 == 0, "stages keep the swizzle's alignment");
-    static_assert(STAGES * STAGE >= NT * ROWS * 4, "the partial sums fit the stages");
+    static_assert(FEW * STAGE >= NT * ROWS * 4, "the partial sums fit the stages");
 };
-constexpr int kBandMaxStages = 6;
+constexpr int kBandMaxStages = 5;
 
 struct BandTail {
     uint64_t full[kBandMaxStages];
@@ -470,8 +475,8 @@ struct BandTail {
     int abort_flag;
 };
 template <int NT>
-constexpr int band_smem() {
-    return Band<NT>::STAGES * Band<NT>::STAGE + (int)sizeof(BandTail);
+constexpr int band_smem(int stages) {
+    return stages * Band<NT>::STAGE + (int)sizeof(BandTail);
 }
 
 struct BArgs {
@@ -481,6 +486,7 @@ struct BArgs {
     int M, N;
     int tiles_k, last_mma;
     int splits;                          // CTAs of a cluster
+    int stages;
     int weights_ready;                   // the weight may be read before griddepcontrol.wait
     uint64_t timeout_ns;
 };
@@ -501,8 +507,9 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                   const BArgs a) {
     using C = Band<NT>;
     static_assert(C::STAGES <= kBandMaxStages, "barriers");
+    const int stages = a.stages;
     extern __shared__ __align__(1024) uint8_t smem[];
-    BandTail *tail = reinterpret_cast<BandTail *>(smem + C::STAGES * C::STAGE);
+    BandTail *tail = reinterpret_cast<BandTail *>(smem + stages * C::STAGE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = a.splits;
     const int rank = (int)(blockIdx.x % (unsigned)S);
@@ -512,8 +519,10 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const int k_begin = (int)((int64_t)a.tiles_k * rank / S);
     const int k_count = (int)((int64_t)a.tiles_k * (rank + 1) / S) - k_begin;
 
+    // the next kernel may set up, and ask L2 for its weight, while this one runs
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; ++s) {
+        for (int s = 0; s < stages; ++s) {
             mbar_init(smem_addr(&tail->full[s]), 1);
             mbar_init(smem_addr(&tail->empty[s]), 1);
         }
@@ -557,38 +566,52 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         if (elect_one()) {
             // Right behind the quantisation of X in one call, the weight does not depend on the
             // kernel that is still running: its first stages are on their way meanwhile.
-            const int pre = a.weights_ready ? min(C::STAGES, k_count) : 0;
+            // Elsewhere that kernel may be writing it: then L2, where every write lands, is asked to
+            // fetch them.
+            const int first = min(stages, k_count);
+            const int pre = a.weights_ready ? first : 0;
             for (int it = 0; it < pre; ++it) load_w(it, it);
+            for (int it = pre; it < first; ++it) {
+                tma_prefetch_l2_2d(&tmW, (k_begin + it) * KB, band * ROWS);
+                tma_prefetch_l2_2d(&tmWS, 0, band * a.tiles_k + k_begin + it);
+            }
             asm volatile("griddepcontrol.wait;" ::: "memory");
             for (int it = 0; it < pre; ++it) load_x(it, it);
-            int issued = pre;
-            for (int it = pre; it < k_count; ++it) {
-                const int stage = it % C::STAGES;
-                if (!wait(smem_addr(&tail->empty[stage]), (uint32_t)(it / C::STAGES + 1) & 1u))
-                    break;
+            int it = pre, stage = pre % stages;
+            uint32_t phase = (uint32_t)(pre / stages);
+            for (; it < k_count; ++it) {
+                if (!wait(smem_addr(&tail->empty[stage]), phase ^ 1)) break;
                 load_w(it, stage);
                 load_x(it, stage);
-                issued = it + 1;
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
             // wait for every copy this thread issued to land before the CTA may exit
-            for (int it = max(0, issued - C::STAGES); it < issued; ++it)
-                drain_wait(smem_addr(&tail->full[it % C::STAGES]), (uint32_t)(it / C::STAGES) & 1u,
+            for (int i = max(0, it - stages); i < it; ++i)
+                drain_wait(smem_addr(&tail->full[i % stages]), (uint32_t)(i / stages) & 1u,
                            a.status);
         }
     } else {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         if (warp == 1 && elect_one()) {
+            int stage = 0;
+            uint32_t phase = 0;
             for (int it = 0; it < k_count; ++it) {
-                const int stage = it % C::STAGES;
-                if (!wait(smem_addr(&tail->full[stage]), (uint32_t)(it / C::STAGES) & 1u)) break;
+                if (!wait(smem_addr(&tail->full[stage]), phase)) break;
                 tc_fence_after();
                 const uint32_t sa = smem_addr(smem + stage * C::STAGE);
                 const uint32_t ss = sa + (ROWS + NT) * KB;
                 mma_ktile<false, ROWS, NT>(tmem, sa, sa + ROWS * KB, ss, ss + kMxTile,
-                                           tmem + C::SF,
+                                           tmem + C::SF, (uint32_t)(m0 & (kMxRows - 1)) >> 5,
                                            k_begin + it == a.tiles_k - 1 ? a.last_mma : 4,
                                            it == 0);
                 tc_commit(smem_addr(&tail->empty[stage]));
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
             // also after a wait that gave up: every MMA issued has completed once this arrives
             tc_commit(smem_addr(&tail->acc_full));
@@ -692,8 +715,9 @@ cudaError_t allow_smem(K kernel, int bytes) {
 
 template <int NT>
 cudaError_t allow_band() {
-    const cudaError_t e = allow_smem(mxfp4_band_kernel<kF16, NT>, band_smem<NT>());
-    return e != cudaSuccess ? e : allow_smem(mxfp4_band_kernel<kBF16, NT>, band_smem<NT>());
+    constexpr int smem = band_smem<NT>(Band<NT>::STAGES);
+    const cudaError_t e = allow_smem(mxfp4_band_kernel<kF16, NT>, smem);
+    return e != cudaSuccess ? e : allow_smem(mxfp4_band_kernel<kBF16, NT>, smem);
 }
 
 // Shared-memory limits, once per device; the SM count.
@@ -711,8 +735,7 @@ cudaError_t device_setup(int *sms) {
             (e = allow_smem(mxfp4_pair_kernel<kF16>, P_SMEM)) != cudaSuccess ||
             (e = allow_smem(mxfp4_pair_kernel<kBF16>, P_SMEM)) != cudaSuccess ||
             (e = allow_band<16>()) != cudaSuccess || (e = allow_band<32>()) != cudaSuccess ||
-            (e = allow_band<64>()) != cudaSuccess || (e = allow_band<128>()) != cudaSuccess ||
-            (e = allow_band<256>()) != cudaSuccess)
+            (e = allow_band<64>()) != cudaSuccess)
             return e;
         known[dev] = n;
     }
@@ -742,18 +765,41 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// The band kernel for tiles of NT rows of X.
 template <int NT>
-cudaError_t band_launch(const Mxfp4Gemm &g, const BArgs &a, cudaStream_t s) {
+cudaError_t band(const Mxfp4Gemm &g, int tiles_k, int last_mma, int sms, cudaStream_t s) {
     Maps t;
     if (!make_maps(&t, g, NT)) return cudaErrorInvalidValue;
+    const int64_t tiles = ceil_div(g.N, ROWS) * ceil_div(g.M, NT);
+    BArgs a;
+    a.bias = g.bias;
+    a.Y = g.Y;
+    a.status = g.status;
+    a.M = (int)g.M;
+    a.N = (int)g.N;
+    a.tiles_k = tiles_k;
+    a.last_mma = last_mma;
+    a.weights_ready = g.weights_ready;
+    a.timeout_ns = g.timeout_ns;
+    // As many splits of k as still leave a CTA an SM of its own and four k-tiles: past that the
+    // exchange costs more than the shorter k saves (1 x 4096 x 4096: 8.4 us in one part, 7.1 in
+    // four, 7.6 in eight; 1 x 1024 x 1024, four k-tiles: 3.8 in one, 4.5 in four).
+    a.splits = (int)std::max<int64_t>(
+        1, std::min<int64_t>({8, sms / tiles, (int64_t)tiles_k / 4}));
+    a.stages = tiles * a.splits > 2 * sms ? Band<NT>::FEW : Band<NT>::STAGES;
     const dim3 grid((unsigned)(ceil_div(g.N, ROWS) * a.splits), (unsigned)ceil_div(g.M, NT));
     auto k = g.dtype == kF16 ? mxfp4_band_kernel<kF16, NT> : mxfp4_band_kernel<kBF16, NT>;
-    return launch_cluster(k, grid, B_THREADS, band_smem<NT>(), a.splits, s, t.X, t.W, t.XS, t.WS,
-                          a);
+    return launch_cluster(k, grid, B_THREADS, band_smem<NT>(a.stages), a.splits, s, t.X, t.W, t.XS,
+                          t.WS, a);
 }
 
-// Rows of X that the band kernel takes.
-constexpr int64_t kBandMaxM = 256;
+// The band kernel takes up to 64 rows of X, and more in tiles of 64 while each tile has an SM of its
+// own.  (us, band / pair: 64 x 49152 x 12288 56.1 / 63.4, 256 x 1024 x 8192 9.0 / 15.3,
+// 128 x 5120 x 5120 11.1 / 11.5; past that rule, 128 x 16384 x 4096 13.0 / 12.1, 256 x 16384 x 4096
+// 18.1 / 12.9, 300 x 4096 x 4096 10.1 / 11.2.)
+bool use_band(int64_t M, int64_t N, int sms) {
+    return M <= 64 || ceil_div(M, 64) * ceil_div(N, ROWS) <= sms;
+}
 
 cudaError_t gemm(const Mxfp4Gemm &g, cudaStream_t s) {
     int sms = 0;
@@ -761,28 +807,10 @@ cudaError_t gemm(const Mxfp4Gemm &g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int tiles_k = (int)ceil_div(g.K, kMxCols);
     const int last_mma = (int)ceil_div(g.K - (int64_t)(tiles_k - 1) * kMxCols, 64);
-    if (g.M <= kBandMaxM) {
-        BArgs a;
-        a.bias = g.bias;
-        a.Y = g.Y;
-        a.status = g.status;
-        a.M = (int)g.M;
-        a.N = (int)g.N;
-        a.tiles_k = tiles_k;
-        a.last_mma = last_mma;
-        a.weights_ready = g.weights_ready;
-        a.timeout_ns = g.timeout_ns;
-        // enough CTAs to fill every SM twice, of at least two k-tiles each
-        const int64_t bands = ceil_div(g.N, ROWS);
-        a.splits = 1;
-        while (a.splits < 8 && bands * a.splits < 2 * sms && tiles_k / (2 * a.splits) >= 2)
-            a.splits *= 2;
-        if (g.M <= 16) return band_launch<16>(g, a, s);
-        if (g.M <= 32) return band_launch<32>(g, a, s);
-        if (g.M <= 64) return band_launch<64>(g, a, s);
-        if (g.M <= 128) return band_launch<128>(g, a, s);
-        return band_launch<256>(g, a, s);
-    }
+    if (use_band(g.M, g.N, sms))
+        return g.M <= 16   ? band<16>(g, tiles_k, last_mma, sms, s)
+               : g.M <= 32 ? band<32>(g, tiles_k, last_mma, sms, s)
+                           : band<64>(g, tiles_k, last_mma, sms, s);
     Maps t;
     if (!make_maps(&t, g, ROWS)) return cudaErrorInvalidValue;
     // rows of Y on 16 bytes are stored by TMA

@@ -122,7 +122,8 @@ def assert_product(y, x, w, b, dtype):
 SHAPES = [(1, 1, 32), (1, 1024, 1024), (2, 130, 64), (5, 129, 96), (16, 512, 4096), (17, 300, 288),
           (33, 128, 544), (64, 257, 1056), (65, 96, 2080), (128, 640, 512), (129, 1000, 320),
           (255, 77, 800), (256, 256, 256), (257, 256, 32), (300, 1003, 2080), (513, 520, 96),
-          (700, 31, 1312), (1000, 2050, 512)]
+          (700, 31, 1312), (1000, 2050, 512), (100, 16000, 96), (1200, 1003, 288),
+          (1300, 2500, 1056)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
@@ -141,7 +142,7 @@ def test_linear(M, N, K, dtype):
     assert torch.equal(y, L.llmint8_mxfp4_linear_quantized(xc, xs, wc, ws, bias=b, dtype=dtype))
 
 
-@pytest.mark.parametrize("M", [9, 100, 400])
+@pytest.mark.parametrize("M", [9, 100, 4000])
 def test_linear_takes_row_pitches_and_leaves_the_rest(M):
     N, K = 333, 288
     big = matrix(M, K + 64, BF16)
@@ -156,7 +157,7 @@ def test_linear_takes_row_pitches_and_leaves_the_rest(M):
     assert L.llmint8_mxfp4_linear(x[:0], wc, ws).shape == (0, N)
 
 
-@pytest.mark.parametrize("M", [4, 300])
+@pytest.mark.parametrize("M", [4, 300, 5000])
 def test_a_row_or_channel_of_nan_stays_alone(M):
     N, K = 200, 320
     x, w, b, _ = layer(M, N, K, F16)
@@ -283,7 +284,7 @@ def block(x, res, w1, w2, a):
     return h, L.llmint8_mxfp4_linear_quantized(c, s, *w2, dtype=x.dtype)
 
 
-@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("M", [1, 40, 300, 1400])
 def test_a_run_of_them_together(M):
     K, N = 512, 1003
     g = torch.Generator().manual_seed(M)
@@ -332,7 +333,7 @@ def test_streams_graphs_and_plans():
     assert torch.equal(plan(), want)
 
     # captured: two products and a norm; replayed on other values of the same buffers
-    big = matrix(300, K, F16, seed=9)
+    big = matrix(2000, K, F16, seed=9, spread=1.0)
     static, static_big = x.clone(), big.clone()
     graph = torch.cuda.CUDAGraph()
     for _ in range(2):
@@ -346,7 +347,7 @@ def test_streams_graphs_and_plans():
     for seed in (1, 2):
         new = matrix(M, K, F16, seed=seed)
         static.copy_(new)
-        static_big.copy_(matrix(300, K, F16, seed=seed + 20))
+        static_big.copy_(matrix(2000, K, F16, seed=seed + 20, spread=1.0))
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, L.llmint8_mxfp4_linear(new, wc, ws, bias=b))
@@ -357,7 +358,7 @@ def test_streams_graphs_and_plans():
 
 def test_two_streams_at_once():
     """Calls that overlap, each with a workspace of its own."""
-    layers = [layer(m, 2048, 2048, F16, seed=m) for m in (8, 200, 600)]
+    layers = [layer(m, 2048, 2048, F16, seed=m) for m in (8, 200, 1500)]
     want = [L.llmint8_mxfp4_linear(x, *q, bias=b) for x, w, b, q in layers]
     streams = [torch.cuda.Stream() for _ in layers]
     for s in streams:
@@ -393,12 +394,12 @@ def test_binding_checks_shapes_and_types():
         L.llmint8_residual_norm(x, norm="batch")
 
 
-@pytest.mark.parametrize("M", [8, 300])
+@pytest.mark.parametrize("M", [8, 1500])
 def test_a_wait_that_runs_out_is_reported(M):
     """A bound of 1 ns makes waits give up: the call ends, says so, and the next one is right.  (The
     few microseconds that a band's waits last may pass before the clock is first read; the
     accumulator of a pair takes tens of them with K = 16384.)"""
-    N, K = (4096, 4096) if M == 8 else (256, 16384)
+    N, K = (4096, 4096) if M == 8 else (1024, 16384)
     x, w, b, (wc, ws) = layer(M, N, K, F16)
     work = torch.empty(L.llmint8_mxfp4_linear_workspace_size(M, N, K), dtype=torch.uint8,
                        device="cuda")
