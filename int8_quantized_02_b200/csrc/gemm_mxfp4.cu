@@ -111,12 +111,9 @@ constexpr int P_STAGES = 6;
 constexpr int P_STAGE = 2 * ROWS * KB + 3 * kMxTile;   // X, half of W, scales of X and of W
 constexpr int P_SHIFT = 224;             // first column of the second accumulator
 constexpr int P_SF = 480;                // first column of the scales
-// Staging of a warp's 32 x 32 outputs: for a TMA store 64 bytes a row with the 64-byte swizzle, or
-// for rows of any alignment 16 outputs a row with a word of padding.
+// Staging of a warp's 32 x 32 outputs, 64 bytes a row in the order of TMA's 64-byte swizzle.
 constexpr int P_STAGE_OUT = 32 * 64;
-constexpr int P_PITCH = 9;
 constexpr int P_STAGING = EPI_WARPS * P_STAGE_OUT;
-static_assert(32 * P_PITCH * 4 <= P_STAGE_OUT, "staging");
 static_assert(P_SHIFT + BN <= P_SF && P_SF + 2 * 12 <= 512, "TMEM columns");
 
 struct PairTail {
@@ -376,40 +373,43 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     p[j] = pack_pair<DT>(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-                if (vec) {
-                    // the warp's last store has read the staging
-                    if (lane == 0) bulk_wait_read();
-                    __syncwarp();
+                // the warp's last stores have read the staging
+                if (vec && lane == 0) bulk_wait_read();
+                __syncwarp();
 #pragma unroll
-                    for (int g = 0; g < 4; ++g)
-                        *reinterpret_cast<uint4 *>(stg + lane * 64 +
-                                                   ((g ^ ((lane >> 1) & 3)) << 4)) =
-                            make_uint4(p[4 * g], p[4 * g + 1], p[4 * g + 2], p[4 * g + 3]);
+                for (int g = 0; g < 4; ++g)
+                    *reinterpret_cast<uint4 *>(stg + lane * 64 + ((g ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(p[4 * g], p[4 * g + 1], p[4 * g + 2], p[4 * g + 3]);
+                if (vec) {
                     fence_proxy_async_shared();
                     __syncwarp();
                     // what lies past M or N is left out by the tensor map
                     if (lane == 0 && m0 < a.M) tma_store_2d(&tmY, smem_addr(stg), nb, m0);
-                } else {
-                    // rows of any alignment: turn 32 rows x 16 columns in shared memory, so that
-                    // half a warp writes 16 neighbouring values of a row
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        __syncwarp();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            reinterpret_cast<uint32_t *>(stg)[lane * P_PITCH + j] = p[g * 8 + j];
-                        __syncwarp();
-                        const int n = nb + g * 16 + (lane & 15);
-#pragma unroll 4
-                        for (int r = 0; r < 32; r += 2) {
-                            const int rr = r + (lane >> 4);
-                            if (n < a.N && m0 + rr < a.M)
-                                static_cast<uint16_t *>(a.Y)[(int64_t)(m0 + rr) * a.N + n] =
-                                    reinterpret_cast<const uint16_t *>(
-                                        stg + rr * P_PITCH * 4)[lane & 15];
-                        }
-                    }
+                    continue;
                 }
+                // rows of any alignment: neighbouring lanes write neighbouring values, in pairs
+                // where rows start on 4 bytes
+                __syncwarp();
+                const int rows = min(32, a.M - m0);
+                uint16_t *y = static_cast<uint16_t *>(a.Y) + (int64_t)m0 * a.N;
+                const auto word_at = [&](int r, int w) {
+                    return stg + r * 64 + (((w >> 2) ^ ((r >> 1) & 3)) << 4) + (w & 3) * 4;
+                };
+                if ((a.N & 1) == 0) {
+                    const int n = nb + 2 * (lane & 15);
+                    if (n < a.N) {
+#pragma unroll 8
+                        for (int r = lane >> 4; r < rows; r += 2)
+                            *reinterpret_cast<uint32_t *>(y + (int64_t)r * a.N + n) =
+                                *reinterpret_cast<const uint32_t *>(word_at(r, lane & 15));
+                    }
+                } else if (nb + lane < a.N) {
+#pragma unroll 8
+                    for (int r = 0; r < rows; ++r)
+                        y[(int64_t)r * a.N + nb + lane] = reinterpret_cast<const uint16_t *>(
+                            word_at(r, lane >> 1))[lane & 1];
+                }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();

@@ -683,11 +683,15 @@ def _linear_args(X, WC, WS, bias, Y, workspace, s):
     M, K, px, ld = _rows(X, _DTYPES16, "X")
     dev, dt = X.device, X.dtype
     N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
-    Y = X.new_empty((M, N)) if Y is None else Y
+    pb = None if bias is None else _arg(bias, dt, (N,), "bias", dev)
+    if Y is None:
+        Y = X.new_empty((M, N))
+        py = Y.data_ptr()
+    else:
+        py = _arg(Y, dt, (M, N), "Y", dev)
     ws = WC.new_empty((llmint8_mxfp4_linear_workspace_size(M, N, K),)) if workspace is None \
         else _workspace(workspace, dev)
-    return Y, ws, (px, DTYPES[dt], M, K, ld, pc, ps, N, _arg(bias, dt, (N,), "bias", dev),
-                   _arg(Y, dt, (M, N), "Y", dev), ws.data_ptr(), ws.numel(), s)
+    return Y, ws, (px, DTYPES[dt], M, K, ld, pc, ps, N, pb, py, ws.data_ptr(), ws.numel(), s)
 
 
 def llmint8_mxfp4_linear(X: torch.Tensor, WC: torch.Tensor, WS: torch.Tensor, bias=None, Y=None,
