@@ -840,13 +840,14 @@ llmint8_status llmint8_residual_norm(const void *X, int dtype, int64_t M, int64_
     a.K = K;
     a.ldx = ldx;
     a.ldr = ldr;
-    a.gate_group = gate ? M / gate_rows : 1;
+    a.gate_group = gate ? (uint32_t)(M / gate_rows) : 1u;
     a.rows_out = align_up(M, 128);
     a.tiles_k = ceil_div(K, 256);
     a.norm = norm;
     a.post_norm = post_norm;
     a.scale = scale;
     a.eps = eps;
+    a.inv_k = 1.0f / (float)K;
     return from_cuda(launch_residual_norm(a, dtype, static_cast<cudaStream_t>(stream)));
 }
 

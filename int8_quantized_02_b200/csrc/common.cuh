@@ -293,6 +293,12 @@ __device__ __forceinline__ void tma_prefetch_l2_2d(const CUtensorMap *tm, int x,
                  : "memory");
 }
 
+// The same for a run of bytes (16-byte aligned, a multiple of 16).
+__device__ __forceinline__ void prefetch_l2(const void *p, int64_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"((uint32_t)bytes)
+                 : "memory");
+}
+
 // ------------------------------------------------------------------- tcgen05 ----------
 __device__ __forceinline__ void tc_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");

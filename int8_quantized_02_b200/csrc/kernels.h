@@ -180,10 +180,10 @@ struct NormArgs {
     void *H, *Y;                         // [M, K] or null
     uint8_t *codes, *scales;             // y as MXFP4, or null
     int64_t M, K, ldx, ldr;
-    int64_t gate_group;                  // rows that share a row of the gate
+    uint32_t gate_group;                 // rows that share a row of the gate
     int64_t rows_out, tiles_k;           // of the scales
     int norm, post_norm;                 // llmint8_norm
-    float scale, eps;
+    float scale, eps, inv_k;             // inv_k = 1 / K
 };
 cudaError_t launch_residual_norm(const NormArgs &a, int dtype, cudaStream_t s);
 

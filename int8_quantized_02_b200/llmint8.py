@@ -538,13 +538,19 @@ _DTYPES16 = (torch.float16, torch.bfloat16)
 _MX_HEADER = 256          # bytes of a workspace that holds a status alone
 
 
-def _run(device: torch.device, stream, call):
-    """call(raw stream), with the device - and the stream, when one is given - current."""
+def _run(device: torch.device, stream, call, *tensors):
+    """call(raw stream), with the device - and the stream, when one is given - current.  `tensors`
+    (None among them) are what the call reads or writes: with a stream of its own, their memory is
+    not handed out again before that stream is done with them."""
     if stream is not None:
         if stream.device != device:
             raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            result = call(stream.cuda_stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return result
     # the handle alone: a Stream object for it costs 3 us, a third of a small call
     index = device.index
     if index == torch.cuda.current_device():
@@ -634,7 +640,7 @@ def llmint8_mxfp4_quantize(X: torch.Tensor, codes=None, scales=None, stream=None
             px, DTYPES[X.dtype], R, K, ld, _arg(c, torch.uint8, c_shape, "codes", dev),
             _arg(t, torch.uint8, s_shape, "scales", dev), s), "llmint8_mxfp4_quantize")
         return c, t
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, X, codes, scales)
 
 
 def llmint8_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor,
@@ -649,7 +655,7 @@ def llmint8_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor,
         _check(load().llmint8_mxfp4_dequant(pc, ps, R, K, _arg(v, dtype, (R, K), "out", dev),
                                             DTYPES[dtype], s), "llmint8_mxfp4_dequant")
         return v
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, codes, scales, out)
 
 
 def _mxfp4_matrix(codes: torch.Tensor, scales: torch.Tensor, c_name: str, s_name: str):
@@ -702,7 +708,7 @@ def llmint8_mxfp4_linear(X: torch.Tensor, WC: torch.Tensor, WS: torch.Tensor, bi
         out, ws, args = _linear_args(X, WC, WS, bias, Y, workspace, s)
         _check(load().llmint8_mxfp4_linear(*args), "llmint8_mxfp4_linear")
         return out
-    return _run(X.device, stream, call)
+    return _run(X.device, stream, call, X, WC, WS, bias, Y, workspace)
 
 
 def llmint8_mxfp4_linear_quantized(XC: torch.Tensor, XS: torch.Tensor, WC: torch.Tensor,
@@ -724,24 +730,29 @@ def llmint8_mxfp4_linear_quantized(XC: torch.Tensor, XS: torch.Tensor, WC: torch
                                                      DTYPES[dtype], ws.data_ptr(), ws.numel(), s),
                "llmint8_mxfp4_linear_quantized")
         return out
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, XC, XS, WC, WS, bias, Y, workspace)
 
 
 class Mxfp4LinearPlan:
     """One llmint8_mxfp4_linear call with its arguments checked and marshalled once (as
-    LinearPlan for the int8 layer): calling the plan runs the layer on the same tensors, which
-    must stay alive and keep their storage while the plan is used.  Made with the tensors' device
-    current, and called with it current."""
+    LinearPlan for the int8 layer): calling the plan runs the layer on the same tensors and the
+    same stream (the one current when it was made, unless one is given).  The tensors must stay
+    alive and keep their storage while the plan is used."""
 
     def __init__(self, X: torch.Tensor, WC: torch.Tensor, WS: torch.Tensor, bias=None, Y=None,
                  workspace=None, stream=None):
         self._keep = (X, WC, WS, bias, stream)
+        self._device = X.device.index
         self._fn = load().llmint8_mxfp4_linear
         self.Y, self.workspace, self._args = _run(
             X.device, stream, lambda s: _linear_args(X, WC, WS, bias, Y, workspace, s))
 
     def __call__(self) -> torch.Tensor:
-        code = self._fn(*self._args)
+        if torch.cuda.current_device() == self._device:
+            code = self._fn(*self._args)
+        else:
+            with torch.cuda.device(self._device):
+                code = self._fn(*self._args)
         if code != OK:
             raise LLMInt8Error(code, "llmint8_mxfp4_linear")
         return self.Y
@@ -787,7 +798,8 @@ def _residual_norm(X, residual, weight, bias, norm, post_norm, post_weight, post
             _arg(c, torch.uint8, c_shape, "codes", dev),
             _arg(t, torch.uint8, s_shape, "scales", dev), s), "llmint8_residual_norm")
         return h, y, c, t
-    return _run(dev, stream, call)
+    return _run(dev, stream, call, X, residual, weight, bias, post_weight, post_bias, gate, H, Y,
+                codes, scales)
 
 
 def llmint8_residual_norm(X: torch.Tensor, residual=None, weight=None, bias=None,
