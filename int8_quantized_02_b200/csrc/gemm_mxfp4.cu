@@ -238,6 +238,8 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 }
             }
         drain:
+            // the next kernel may set up while the last tiles are finished
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             // Every copy that signals the leader's barriers lands before either CTA exits.  After a
             // wait that gave up, one CTA may have issued k-tiles that the other did not: the
             // leader then takes the missing copies' bytes off, or expects those it did not.
