@@ -700,10 +700,13 @@ llmint8_status check_mxfp4(int dtype, int64_t M, int64_t K, const uint8_t *Wc, c
 }
 
 // The product between the process-wide profile events (when set).
-llmint8_status run_mxfp4(const uint8_t *Xc, const uint8_t *Xs, int64_t M, int64_t K,
-                         const uint8_t *Wc, const uint8_t *Ws, int64_t N, const void *bias,
-                         void *Y, int dtype, int weights_ready, void *ws, cudaStream_t s) {
+llmint8_status run_mxfp4(const void *X, int64_t ldx, const uint8_t *Xc, const uint8_t *Xs,
+                         int64_t M, int64_t K, const uint8_t *Wc, const uint8_t *Ws, int64_t N,
+                         const void *bias, void *Y, int dtype, int weights_ready, void *ws,
+                         cudaStream_t s) {
     Mxfp4Gemm g;
+    g.X = X;
+    g.ldx = ldx;
     g.Xc = Xc;
     g.Xs = Xs;
     g.Wc = Wc;
@@ -777,13 +780,15 @@ llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t
     if (M == 0) return LLMINT8_OK;
     if (!X || !aligned16(X) || !pitch_ok(ldx, K, 2)) return LLMINT8_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (mxfp4_fused(M, N, K))
+        return run_mxfp4(X, ldx, nullptr, nullptr, M, K, Wc, Ws, N, bias, Y, dtype, 0, ws, s);
     const Mxfp4Layout L = mxfp4_layout(M, K);
     uint8_t *Xc = at<uint8_t>(ws, L.codes), *Xs = at<uint8_t>(ws, L.scales);
     // rows past M of the last scale tile meet only codes that read as zero, in columns of the
     // product that are not stored: they stay as they are
     if (launch_mxfp4_quantize(X, dtype, ldx, M, false, K, Xc, Xs, s) != cudaSuccess)
         return LLMINT8_ERR_CUDA;
-    return run_mxfp4(Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 1, ws, s);
+    return run_mxfp4(nullptr, 0, Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 1, ws, s);
 }
 
 llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, const uint8_t *Xs, int64_t M,
@@ -796,7 +801,7 @@ llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, const uint8_t *
     if (chk != LLMINT8_OK) return chk;
     if (M == 0) return LLMINT8_OK;
     if (!mx_pair_ok(Xc, Xs)) return LLMINT8_ERR_INVALID_ARG;
-    return run_mxfp4(Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 0, ws,
+    return run_mxfp4(nullptr, 0, Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 0, ws,
                      static_cast<cudaStream_t>(stream));
 }
 

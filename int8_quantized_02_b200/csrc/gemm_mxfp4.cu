@@ -20,6 +20,9 @@
 //         columns, so each weight byte enters one SM once.  The k range of a band of 128 weight
 //         rows is split over the S CTAs of a cluster, which add their partial sums through
 //         distributed shared memory in rank order (the result does not depend on timing).
+//         With up to 8 rows and little of k to a CTA, X comes unquantised: the epilogue's warps
+//         quantise each k-tile's rows straight into its stage, in turns, and the layer is one
+//         launch.
 // Every wait on an mbarrier is bounded (BoundedWait), as in the int8 product.
 #include <mutex>
 
@@ -447,6 +450,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 
 // ------------------------------------------------------------------------- band ---------
 constexpr int B_THREADS = 192;           // producer, MMA issuer, four epilogue warps
+constexpr int kFusedRows = 8;            // rows of X that the kernel quantises itself at most
 
 template <int NT>
 struct Band {
@@ -470,7 +474,8 @@ struct Band {
 constexpr int kBandMaxStages = 5;
 
 struct BandTail {
-    uint64_t full[kBandMaxStages];
+    uint64_t full[kBandMaxStages];       // the copies into a stage have landed
+    uint64_t quantised[kBandMaxStages];  // fused: X's rows are in it
     uint64_t empty[kBandMaxStages];
     uint64_t acc_full;
     uint32_t tmem_base;
@@ -482,6 +487,9 @@ constexpr int band_smem(int stages) {
 }
 
 struct BArgs {
+    const uint8_t *X;                    // fused: X itself, its row pitch in bytes, chunks of a row
+    int64_t row_bytes;
+    int64_t chunks;
     const void *bias;
     void *Y;
     StatusRef status;
@@ -502,7 +510,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-template <int DT, int NT>
+template <int DT, int NT, bool FUSED>
 __global__ void __launch_bounds__(B_THREADS)
 mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                   const __grid_constant__ CUtensorMap tmXS, const __grid_constant__ CUtensorMap tmWS,
@@ -526,15 +534,18 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(smem_addr(&tail->full[s]), 1);
+            mbar_init(smem_addr(&tail->quantised[s]), 1);
             mbar_init(smem_addr(&tail->empty[s]), 1);
         }
         mbar_init(smem_addr(&tail->acc_full), 1);
         tail->abort_flag = 0;
         fence_mbar_init();
-        tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmW);
-        tma_prefetch_desc(&tmXS);
         tma_prefetch_desc(&tmWS);
+        if (!FUSED) {
+            tma_prefetch_desc(&tmX);
+            tma_prefetch_desc(&tmXS);
+        }
     }
     if (warp == 1) tmem_alloc(smem_addr(&tail->tmem_base), C::COLS);
     tc_fence_before();
@@ -548,11 +559,12 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         const uint32_t full = smem_addr(&tail->full[stage]);
         const uint32_t sa = smem_addr(smem + stage * C::STAGE);
         const int kt = k_begin + it;
-        mbar_arrive_expect_tx(full, C::STAGE);
+        mbar_arrive_expect_tx(full, FUSED ? ROWS * KB + kMxTile : C::STAGE);
         tma_load_2d(sa, &tmW, kt * KB, band * ROWS, full);
         tma_load_2d(sa + (ROWS + NT) * KB, &tmWS, 0, band * a.tiles_k + kt, full);
     };
     auto load_x = [&](int it, int stage) {
+        if (FUSED) return;
         const uint32_t full = smem_addr(&tail->full[stage]);
         const uint32_t sa = smem_addr(smem + stage * C::STAGE);
         const int kt = k_begin + it;
@@ -602,6 +614,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             uint32_t phase = 0;
             for (int it = 0; it < k_count; ++it) {
                 if (!wait(smem_addr(&tail->full[stage]), phase)) break;
+                if (FUSED && !wait(smem_addr(&tail->quantised[stage]), phase)) break;
                 tc_fence_after();
                 const uint32_t sa = smem_addr(smem + stage * C::STAGE);
                 const uint32_t ss = sa + (ROWS + NT) * KB;
@@ -618,6 +631,41 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             // also after a wait that gave up: every MMA issued has completed once this arrives
             tc_commit(smem_addr(&tail->acc_full));
             drain_wait(smem_addr(&tail->acc_full), 0, a.status);
+        }
+        // Every `turns`-th k-tile is a warp's: X's rows to codes (a row of the swizzled operand, 16-byte
+        // pieces XOR the row) and scales (a word a half tile), as the copies would have left them.
+        // No more turns than stages: a warp that waits for stage k-tile `it` then knows that the
+        // k-tile before the one there was consumed, so the barrier's parity tells the two apart.
+        const int turns = min(4, stages);
+        if (FUSED && warp >= 2 && warp - 2 < turns) {
+            for (int it = warp - 2; it < k_count; it += turns) {
+                const int stage = it % stages;
+                const int64_t kt = k_begin + it, ch = kt * 32 + lane;
+                Chunk<DT> c[kFusedRows];
+#pragma unroll
+                for (int m = 0; m < kFusedRows; ++m)
+                    c[m] = m < a.M && ch < a.chunks ? load_chunk<DT>(a.X + m * a.row_bytes, ch)
+                                                    : zero_chunk<DT>();
+                int ok = 0;
+                if (lane == 0)
+                    ok = wait(smem_addr(&tail->empty[stage]), (uint32_t)(it / stages + 1) & 1u);
+                if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+                uint8_t *sx = smem + stage * C::STAGE + ROWS * KB;
+                uint8_t *ss = sx + NT * KB + kMxTile;
+#pragma unroll
+                for (int m = 0; m < kFusedRows; ++m) {
+                    if (m >= a.M) break;
+                    uint32_t word;
+                    const uint32_t q = quantize_chunk<DT>(c[m], word, lane);
+                    *reinterpret_cast<uint32_t *>(sx + m * KB + (((lane >> 2) ^ m) << 4) +
+                                                  (lane & 3) * 4) = q;
+                    if ((lane & 15) == 0)
+                        *reinterpret_cast<uint32_t *>(ss + (lane >> 4) * 512 + m * 16) = word;
+                }
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&tail->quantised[stage]));
+            }
         }
     }
     __syncwarp();
@@ -697,15 +745,17 @@ struct Maps {
     CUtensorMap X, W, XS, WS;
 };
 
-bool make_maps(Maps *t, const Mxfp4Gemm &g, uint32_t x_rows) {
+bool make_maps(Maps *t, const Mxfp4Gemm &g, uint32_t x_rows, bool fused = false) {
     const int64_t tiles_k = ceil_div(g.K, kMxCols);
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     const auto u32 = CU_TENSOR_MAP_DATA_TYPE_UINT32;
     const auto flat = CU_TENSOR_MAP_SWIZZLE_NONE;
-    return make_map(&t->X, g.Xc, u8, 1, g.K / 2, g.M, g.K / 2, KB, x_rows) &&
+    if (fused) memset(t, 0, sizeof(*t));
+    return (fused ||
+            (make_map(&t->X, g.Xc, u8, 1, g.K / 2, g.M, g.K / 2, KB, x_rows) &&
+             make_map(&t->XS, g.Xs, u32, 4, kMxTile / 4, ceil_div(g.M, kMxRows) * tiles_k,
+                      kMxTile / 4, kMxTile / 4, 1, flat))) &&
            make_map(&t->W, g.Wc, u8, 1, g.K / 2, g.N, g.K / 2, KB, ROWS) &&
-           make_map(&t->XS, g.Xs, u32, 4, kMxTile / 4, ceil_div(g.M, kMxRows) * tiles_k,
-                    kMxTile / 4, kMxTile / 4, 1, flat) &&
            make_map(&t->WS, g.Ws, u32, 4, kMxTile / 4, ceil_div(g.N, kMxRows) * tiles_k,
                     kMxTile / 4, kMxTile / 4, 1, flat);
 }
@@ -718,8 +768,13 @@ cudaError_t allow_smem(K kernel, int bytes) {
 template <int NT>
 cudaError_t allow_band() {
     constexpr int smem = band_smem<NT>(Band<NT>::STAGES);
-    const cudaError_t e = allow_smem(mxfp4_band_kernel<kF16, NT>, smem);
-    return e != cudaSuccess ? e : allow_smem(mxfp4_band_kernel<kBF16, NT>, smem);
+    cudaError_t e = allow_smem(mxfp4_band_kernel<kF16, NT, false>, smem);
+    if (e == cudaSuccess) e = allow_smem(mxfp4_band_kernel<kBF16, NT, false>, smem);
+    if constexpr (NT == 16) {
+        if (e == cudaSuccess) e = allow_smem(mxfp4_band_kernel<kF16, NT, true>, smem);
+        if (e == cudaSuccess) e = allow_smem(mxfp4_band_kernel<kBF16, NT, true>, smem);
+    }
+    return e;
 }
 
 // Shared-memory limits, once per device; the SM count.
@@ -767,13 +822,24 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, int
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// CTAs that share a band's k.  As many as still leave each an SM of its own and four k-tiles: past
+// that the exchange costs more than the shorter k saves (1 x 4096 x 4096: 8.4 us in one part, 7.1 in
+// four, 7.6 in eight; 1 x 1024 x 1024, four k-tiles: 3.8 in one, 4.5 in four).
+int band_splits(int64_t tiles, int tiles_k, int sms) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({8, sms / tiles, (int64_t)tiles_k / 4}));
+}
+
 // The band kernel for tiles of NT rows of X.
 template <int NT>
 cudaError_t band(const Mxfp4Gemm &g, int tiles_k, int last_mma, int sms, cudaStream_t s) {
+    const bool fused = g.X != nullptr;
     Maps t;
-    if (!make_maps(&t, g, NT)) return cudaErrorInvalidValue;
+    if (!make_maps(&t, g, NT, fused)) return cudaErrorInvalidValue;
     const int64_t tiles = ceil_div(g.N, ROWS) * ceil_div(g.M, NT);
     BArgs a;
+    a.X = static_cast<const uint8_t *>(g.X);
+    a.row_bytes = g.ldx * 2;
+    a.chunks = g.K / 8;
     a.bias = g.bias;
     a.Y = g.Y;
     a.status = g.status;
@@ -783,14 +849,16 @@ cudaError_t band(const Mxfp4Gemm &g, int tiles_k, int last_mma, int sms, cudaStr
     a.last_mma = last_mma;
     a.weights_ready = g.weights_ready;
     a.timeout_ns = g.timeout_ns;
-    // As many splits of k as still leave a CTA an SM of its own and four k-tiles: past that the
-    // exchange costs more than the shorter k saves (1 x 4096 x 4096: 8.4 us in one part, 7.1 in
-    // four, 7.6 in eight; 1 x 1024 x 1024, four k-tiles: 3.8 in one, 4.5 in four).
-    a.splits = (int)std::max<int64_t>(
-        1, std::min<int64_t>({8, sms / tiles, (int64_t)tiles_k / 4}));
+    a.splits = band_splits(tiles, tiles_k, sms);
     a.stages = tiles * a.splits > 2 * sms ? Band<NT>::FEW : Band<NT>::STAGES;
     const dim3 grid((unsigned)(ceil_div(g.N, ROWS) * a.splits), (unsigned)ceil_div(g.M, NT));
-    auto k = g.dtype == kF16 ? mxfp4_band_kernel<kF16, NT> : mxfp4_band_kernel<kBF16, NT>;
+    auto k = g.dtype == kF16 ? mxfp4_band_kernel<kF16, NT, false>
+                             : mxfp4_band_kernel<kBF16, NT, false>;
+    if constexpr (NT == 16) {
+        if (fused)
+            k = g.dtype == kF16 ? mxfp4_band_kernel<kF16, NT, true>
+                                : mxfp4_band_kernel<kBF16, NT, true>;
+    }
     return launch_cluster(k, grid, B_THREADS, band_smem<NT>(a.stages), a.splits, s, t.X, t.W, t.XS,
                           t.WS, a);
 }
@@ -802,6 +870,10 @@ cudaError_t band(const Mxfp4Gemm &g, int tiles_k, int last_mma, int sms, cudaStr
 bool use_band(int64_t M, int64_t N, int sms) {
     return M <= 64 || ceil_div(M, 64) * ceil_div(N, ROWS) <= sms;
 }
+
+// Rows times k-tiles that a CTA quantises itself at most: every CTA does this work, and past it the
+// launch that quantises X once is the shorter way.
+constexpr int64_t kFusedWork = 64;
 
 cudaError_t gemm(const Mxfp4Gemm &g, cudaStream_t s) {
     int sms = 0;
@@ -844,6 +916,14 @@ cudaError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, cudaStream_t s) {
     const cudaError_t e = gemm(g, s);
     note_launches(1);
     return e;
+}
+
+bool mxfp4_fused(int64_t M, int64_t N, int64_t K) {
+    int sms = 0;
+    if (M > kFusedRows || device_setup(&sms) != cudaSuccess) return false;
+    const int tiles_k = (int)ceil_div(K, kMxCols);
+    const int64_t per_cta = ceil_div(tiles_k, band_splits(ceil_div(N, ROWS), tiles_k, sms));
+    return M * per_cta <= kFusedWork;
 }
 
 }  // namespace llmint8
