@@ -780,7 +780,7 @@ llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t
     if (M == 0) return LLMINT8_OK;
     if (!X || !aligned16(X) || !pitch_ok(ldx, K, 2)) return LLMINT8_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (mxfp4_fused(M, N, K))
+    if (M <= kMxfp4FusedRows)
         return run_mxfp4(X, ldx, nullptr, nullptr, M, K, Wc, Ws, N, bias, Y, dtype, 0, ws, s);
     const Mxfp4Layout L = mxfp4_layout(M, K);
     uint8_t *Xc = at<uint8_t>(ws, L.codes), *Xs = at<uint8_t>(ws, L.scales);

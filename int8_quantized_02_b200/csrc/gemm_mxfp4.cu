@@ -20,9 +20,11 @@
 //         columns, so each weight byte enters one SM once.  The k range of a band of 128 weight
 //         rows is split over the S CTAs of a cluster, which add their partial sums through
 //         distributed shared memory in rank order (the result does not depend on timing).
-//         With up to 8 rows and little of k to a CTA, X comes unquantised: the epilogue's warps
-//         quantise each k-tile's rows straight into its stage, in turns, and the layer is one
-//         launch.
+//         Up to 8 rows of X come unquantised: the epilogue's warps quantise each k-tile's rows
+//         straight into its stage, in turns, while the weight streams in, and the layer is one
+//         launch (us, one / two launches: 1 x 4096 x 4096 5.0 / 7.2, 8 x 16384 x 4096 10.3 / 11.8,
+//         8 x 49152 x 12288 50.8 / 52.5; 16 rows do not fit the time that a k-tile of the weight
+//         takes, 16 x 16384 x 4096 17.1 / 11.9).
 // Every wait on an mbarrier is bounded (BoundedWait), as in the int8 product.
 #include <mutex>
 
@@ -450,7 +452,6 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 
 // ------------------------------------------------------------------------- band ---------
 constexpr int B_THREADS = 192;           // producer, MMA issuer, four epilogue warps
-constexpr int kFusedRows = 8;            // rows of X that the kernel quantises itself at most
 
 template <int NT>
 struct Band {
@@ -517,6 +518,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                   const BArgs a) {
     using C = Band<NT>;
     static_assert(C::STAGES <= kBandMaxStages, "barriers");
+    static_assert(!FUSED || (NT >= kMxfp4FusedRows && kMxfp4FusedRows <= 8), "rows of one swizzle atom");
     const int stages = a.stages;
     extern __shared__ __align__(1024) uint8_t smem[];
     BandTail *tail = reinterpret_cast<BandTail *>(smem + stages * C::STAGE);
@@ -641,9 +643,9 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             for (int it = warp - 2; it < k_count; it += turns) {
                 const int stage = it % stages;
                 const int64_t kt = k_begin + it, ch = kt * 32 + lane;
-                Chunk<DT> c[kFusedRows];
+                Chunk<DT> c[kMxfp4FusedRows];
 #pragma unroll
-                for (int m = 0; m < kFusedRows; ++m)
+                for (int m = 0; m < kMxfp4FusedRows; ++m)
                     c[m] = m < a.M && ch < a.chunks ? load_chunk<DT>(a.X + m * a.row_bytes, ch)
                                                     : zero_chunk<DT>();
                 int ok = 0;
@@ -653,7 +655,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 uint8_t *sx = smem + stage * C::STAGE + ROWS * KB;
                 uint8_t *ss = sx + NT * KB + kMxTile;
 #pragma unroll
-                for (int m = 0; m < kFusedRows; ++m) {
+                for (int m = 0; m < kMxfp4FusedRows; ++m) {
                     if (m >= a.M) break;
                     uint32_t word;
                     const uint32_t q = quantize_chunk<DT>(c[m], word, lane);
@@ -871,10 +873,6 @@ bool use_band(int64_t M, int64_t N, int sms) {
     return M <= 64 || ceil_div(M, 64) * ceil_div(N, ROWS) <= sms;
 }
 
-// Rows times k-tiles that a CTA quantises itself at most: every CTA does this work, and past it the
-// launch that quantises X once is the shorter way.
-constexpr int64_t kFusedWork = 64;
-
 cudaError_t gemm(const Mxfp4Gemm &g, cudaStream_t s) {
     int sms = 0;
     cudaError_t e = device_setup(&sms);
@@ -916,14 +914,6 @@ cudaError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, cudaStream_t s) {
     const cudaError_t e = gemm(g, s);
     note_launches(1);
     return e;
-}
-
-bool mxfp4_fused(int64_t M, int64_t N, int64_t K) {
-    int sms = 0;
-    if (M > kFusedRows || device_setup(&sms) != cudaSuccess) return false;
-    const int tiles_k = (int)ceil_div(K, kMxCols);
-    const int64_t per_cta = ceil_div(tiles_k, band_splits(ceil_div(N, ROWS), tiles_k, sms));
-    return M * per_cta <= kFusedWork;
 }
 
 }  // namespace llmint8

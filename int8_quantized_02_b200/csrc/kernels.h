@@ -157,9 +157,10 @@ cudaError_t launch_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, in
                                  int64_t K, void *out, int dtype, cudaStream_t s);
 
 // The MXFP4 product (gemm_mxfp4.cu).
+constexpr int kMxfp4FusedRows = 8;       // rows of X that the product quantises itself at most
 struct Mxfp4Gemm {
-    const void *X;           // [M, K] of dtype, rows ldx apart, to be quantised in the kernel where
-    int64_t ldx;             // mxfp4_fused() allows it; else null, and
+    const void *X;           // [M, K] of dtype, rows ldx apart, to be quantised in the kernel
+    int64_t ldx;             // (M <= kMxfp4FusedRows); or null, and
     const uint8_t *Xc, *Xs;  // X [M, K] as MXFP4
     const uint8_t *Wc, *Ws;  // W [N, K]
     const void *bias;        // [N] or null
@@ -171,8 +172,6 @@ struct Mxfp4Gemm {
     uint64_t timeout_ns;
 };
 cudaError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, cudaStream_t s);
-// Whether the product quantises X itself, in one launch (on the current device).
-bool mxfp4_fused(int64_t M, int64_t N, int64_t K);
 
 // The residual norm (norm.cu).
 constexpr int64_t kNormMaxK = 32768;

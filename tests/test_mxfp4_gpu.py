@@ -119,7 +119,7 @@ def assert_product(y, x, w, b, dtype):
     assert (off <= tol).all(), (off / tol).max()
 
 
-SHAPES = [(1, 1, 32), (1, 130, 131072), (3, 200, 8224), (7, 96, 2080), (8, 130, 4096), (8, 257, 16416), (1, 1024, 1024), (2, 130, 64), (5, 129, 96), (16, 512, 4096), (17, 300, 288),
+SHAPES = [(1, 1, 32), (1, 130, 131072), (3, 200, 8224), (7, 96, 2080), (8, 130, 4096), (8, 257, 16416), (9, 300, 4128), (15, 1000, 2080), (1, 1024, 1024), (2, 130, 64), (5, 129, 96), (16, 512, 4096), (17, 300, 288),
           (33, 128, 544), (64, 257, 1056), (65, 96, 2080), (128, 640, 512), (129, 1000, 320),
           (255, 77, 800), (256, 256, 256), (257, 256, 32), (300, 1003, 2080), (513, 520, 96),
           (700, 31, 1312), (1000, 2050, 512), (100, 16000, 96), (1200, 1003, 288),
