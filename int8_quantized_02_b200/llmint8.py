@@ -592,6 +592,14 @@ def _arg(t: torch.Tensor | None, dtype: torch.dtype, shape, name: str, device: t
     return t.data_ptr()
 
 
+def _out(t: torch.Tensor | None, like: torch.Tensor, dtype: torch.dtype, shape, name: str):
+    """(tensor, address) of an output: the one given, or a new one on `like`'s device."""
+    if t is None:
+        t = like.new_empty(shape, dtype=dtype)
+        return t, t.data_ptr()
+    return t, _arg(t, dtype, shape, name, like.device)
+
+
 def mxfp4_scales_shape(R: int, K: int) -> tuple[int, int, int]:
     """Shape of the scales of an MXFP4 matrix of R rows and K columns (tiles of 128 x 256)."""
     return (R + 127) // 128, (K + 255) // 256, 1024
@@ -634,11 +642,10 @@ def llmint8_mxfp4_quantize(X: torch.Tensor, codes=None, scales=None, stream=None
     c_shape, s_shape = (R, K // 2), mxfp4_scales_shape(R, K)
 
     def call(s):
-        c = X.new_empty(c_shape, dtype=torch.uint8) if codes is None else codes
-        t = X.new_empty(s_shape, dtype=torch.uint8) if scales is None else scales
-        _check(load().llmint8_mxfp4_quantize(
-            px, DTYPES[X.dtype], R, K, ld, _arg(c, torch.uint8, c_shape, "codes", dev),
-            _arg(t, torch.uint8, s_shape, "scales", dev), s), "llmint8_mxfp4_quantize")
+        c, pc = _out(codes, X, torch.uint8, c_shape, "codes")
+        t, pt = _out(scales, X, torch.uint8, s_shape, "scales")
+        _check(load().llmint8_mxfp4_quantize(px, DTYPES[X.dtype], R, K, ld, pc, pt, s),
+               "llmint8_mxfp4_quantize")
         return c, t
     return _run(dev, stream, call, X, codes, scales)
 
@@ -651,9 +658,9 @@ def llmint8_mxfp4_dequant(codes: torch.Tensor, scales: torch.Tensor,
         raise TypeError(f"dtype must be one of {', '.join(map(str, DTYPES))}, got {dtype}")
 
     def call(s):
-        v = codes.new_empty((R, K), dtype=dtype) if out is None else out
-        _check(load().llmint8_mxfp4_dequant(pc, ps, R, K, _arg(v, dtype, (R, K), "out", dev),
-                                            DTYPES[dtype], s), "llmint8_mxfp4_dequant")
+        v, pv = _out(out, codes, dtype, (R, K), "out")
+        _check(load().llmint8_mxfp4_dequant(pc, ps, R, K, pv, DTYPES[dtype], s),
+               "llmint8_mxfp4_dequant")
         return v
     return _run(dev, stream, call, codes, scales, out)
 
@@ -689,12 +696,8 @@ def _linear_args(X, WC, WS, bias, Y, workspace, s):
     M, K, px, ld = _rows(X, _DTYPES16, "X")
     dev, dt = X.device, X.dtype
     N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
-    pb = None if bias is None else _arg(bias, dt, (N,), "bias", dev)
-    if Y is None:
-        Y = X.new_empty((M, N))
-        py = Y.data_ptr()
-    else:
-        py = _arg(Y, dt, (M, N), "Y", dev)
+    pb = _arg(bias, dt, (N,), "bias", dev)
+    Y, py = _out(Y, X, dt, (M, N), "Y")
     ws = WC.new_empty((llmint8_mxfp4_linear_workspace_size(M, N, K),)) if workspace is None \
         else _workspace(workspace, dev)
     return Y, ws, (px, DTYPES[dt], M, K, ld, pc, ps, N, pb, py, ws.data_ptr(), ws.numel(), s)
@@ -723,11 +726,10 @@ def llmint8_mxfp4_linear_quantized(XC: torch.Tensor, XS: torch.Tensor, WC: torch
     pb = _arg(bias, dtype, (N,), "bias", dev)
 
     def call(s):
-        out = XC.new_empty((M, N), dtype=dtype) if Y is None else Y
+        out, py = _out(Y, XC, dtype, (M, N), "Y")
         ws = XC.new_empty((_MX_HEADER,)) if workspace is None else _workspace(workspace, dev)
-        _check(load().llmint8_mxfp4_linear_quantized(xc, xs, M, K, pc, ps, N, pb,
-                                                     _arg(out, dtype, (M, N), "Y", dev),
-                                                     DTYPES[dtype], ws.data_ptr(), ws.numel(), s),
+        _check(load().llmint8_mxfp4_linear_quantized(xc, xs, M, K, pc, ps, N, pb, py, DTYPES[dtype],
+                                                     ws.data_ptr(), ws.numel(), s),
                "llmint8_mxfp4_linear_quantized")
         return out
     return _run(dev, stream, call, XC, XS, WC, WS, bias, Y, workspace)
@@ -777,26 +779,21 @@ def _residual_norm(X, residual, weight, bias, norm, post_norm, post_weight, post
         if G < 1 or M % G:
             raise ValueError(f"the gate's {G} rows must divide X's {M}")
         pg = _arg(gate, dt, (G, K), "gate", dev)
-    vec = (K,)
-    pw, pb = _arg(weight, dt, vec, "weight", dev), _arg(bias, dt, vec, "bias", dev)
-    ppw = _arg(post_weight, dt, vec, "post_weight", dev)
-    ppb = _arg(post_bias, dt, vec, "post_bias", dev)
-    c_shape, s_shape = (M, K // 2), mxfp4_scales_shape(M, K)
+    pw, pb = _arg(weight, dt, (K,), "weight", dev), _arg(bias, dt, (K,), "bias", dev)
+    ppw = _arg(post_weight, dt, (K,), "post_weight", dev)
+    ppb = _arg(post_bias, dt, (K,), "post_bias", dev)
 
     def call(s):
-        h = X.new_empty((M, K)) if H is None else H
-        y, c, t = Y, codes, scales
-        if want_y and y is None:
-            y = X.new_empty((M, K))
-        if want_codes and c is None:
-            c = X.new_empty(c_shape, dtype=torch.uint8)
-        if want_codes and t is None:
-            t = X.new_empty(s_shape, dtype=torch.uint8)
-        _check(load().llmint8_residual_norm(
-            px, DTYPES[dt], M, K, ld, pr, ldr, NORMS[post_norm], ppw, ppb, pg, G, scale,
-            NORMS[norm], pw, pb, eps, _arg(h, dt, (M, K), "H", dev), _arg(y, dt, (M, K), "Y", dev),
-            _arg(c, torch.uint8, c_shape, "codes", dev),
-            _arg(t, torch.uint8, s_shape, "scales", dev), s), "llmint8_residual_norm")
+        h, ph = _out(H, X, dt, (M, K), "H")
+        y = py = c = pc = t = pt = None
+        if want_y:
+            y, py = _out(Y, X, dt, (M, K), "Y")
+        if want_codes:
+            c, pc = _out(codes, X, torch.uint8, (M, K // 2), "codes")
+            t, pt = _out(scales, X, torch.uint8, mxfp4_scales_shape(M, K), "scales")
+        _check(load().llmint8_residual_norm(px, DTYPES[dt], M, K, ld, pr, ldr, NORMS[post_norm],
+                                            ppw, ppb, pg, G, scale, NORMS[norm], pw, pb, eps, ph,
+                                            py, pc, pt, s), "llmint8_residual_norm")
         return h, y, c, t
     return _run(dev, stream, call, X, residual, weight, bias, post_weight, post_bias, gate, H, Y,
                 codes, scales)
