@@ -661,9 +661,9 @@ namespace {
 bool mx_k_ok(int64_t K) { return K >= 32 && K % 32 == 0 && K <= 131072; }
 bool mx_rows_ok(int64_t R) { return R >= 0 && R <= (int64_t)INT32_MAX; }
 bool dtype16(int dtype) { return dtype == LLMINT8_F16 || dtype == LLMINT8_BF16; }
-// A row pitch of `ld` elements of `bytes` bytes: at least K, each row on 16 bytes.
+// A row pitch of `ld` elements of `bytes` bytes: K to 2^30 elements, each row on 16 bytes.
 bool pitch_ok(int64_t ld, int64_t K, int bytes) {
-    return ld >= K && ld <= INT64_MAX / 16 && ld * bytes % 16 == 0;
+    return ld >= K && ld <= ((int64_t)1 << 30) && ld * bytes % 16 == 0;
 }
 bool mx_pair_ok(const uint8_t *codes, const uint8_t *scales) {
     return codes && scales && aligned16(codes) && aligned16(scales);
@@ -841,13 +841,13 @@ llmint8_status llmint8_residual_norm(const void *X, int dtype, int64_t M, int64_
     a.Y = Y;
     a.codes = codes;
     a.scales = scales;
-    a.M = M;
-    a.K = K;
-    a.ldx = ldx;
-    a.ldr = ldr;
+    a.x_pitch = (uint32_t)(ldx * 2);
+    a.r_pitch = residual ? (uint32_t)(ldr * 2) : 0u;
+    a.pitch = (uint32_t)(K * 2);
+    a.M = (uint32_t)M;
     a.gate_group = gate ? (uint32_t)(M / gate_rows) : 1u;
-    a.rows_out = align_up(M, 128);
-    a.tiles_k = ceil_div(K, 256);
+    a.rows_out = (uint32_t)align_up(M, 128);
+    a.tiles_k = (uint32_t)ceil_div(K, 256);
     a.norm = norm;
     a.post_norm = post_norm;
     a.scale = scale;

@@ -176,15 +176,16 @@ cudaError_t launch_mxfp4_gemm(const Mxfp4Gemm &g, cudaStream_t s);
 // The residual norm (norm.cu).
 constexpr int64_t kNormMaxK = 32768;
 struct NormArgs {
-    const void *X, *residual;            // [M, K], row pitches ldx, ldr; residual may be null
+    const void *X, *residual;            // [M, K]; residual may be null
     const void *post_weight, *post_bias; // [K] or null
     const void *gate;                    // [M / gate_group, K] or null
     const void *weight, *bias;           // [K] or null
     void *H, *Y;                         // [M, K] or null
     uint8_t *codes, *scales;             // y as MXFP4, or null
-    int64_t M, K, ldx, ldr;
+    uint32_t x_pitch, r_pitch, pitch;    // bytes from row to row: X, residual, dense rows (2 K)
+    uint32_t M;
     uint32_t gate_group;                 // rows that share a row of the gate
-    int64_t rows_out, tiles_k;           // of the scales
+    uint32_t rows_out, tiles_k;          // of the scales
     int norm, post_norm;                 // llmint8_norm
     float scale, eps, inv_k;             // inv_k = 1 / K
 };

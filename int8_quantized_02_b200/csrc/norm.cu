@@ -73,14 +73,14 @@ __device__ __forceinline__ void row_norm(const float (&v)[NCH][8], const bool (&
 // v = (v - mean) * rstd * w + b over one chunk; w and b may be null.
 template <int DT>
 __device__ __forceinline__ void apply_norm(float (&v)[8], int kind, float mean, float rstd,
-                                           const void *w, const void *b, int64_t ch) {
+                                           const uint8_t *w, const uint8_t *b) {
     if (kind == LLMINT8_NORM_LAYER) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] -= mean;
     }
     float t[8];
     if (w) {
-        unpack_chunk<DT>(load_chunk<DT>(w, ch), t);
+        unpack_chunk<DT>(load_chunk<DT>(w, 0), t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] *= rstd * t[e];
     } else {
@@ -88,45 +88,54 @@ __device__ __forceinline__ void apply_norm(float (&v)[8], int kind, float mean, 
         for (int e = 0; e < 8; ++e) v[e] *= rstd;
     }
     if (b) {
-        unpack_chunk<DT>(load_chunk<DT>(b, ch), t);
+        unpack_chunk<DT>(load_chunk<DT>(b, 0), t);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] += t[e];
     }
 }
 
+// A thread's share of an array with rows: its first chunk of row `row`.
+__device__ __forceinline__ const uint8_t *share(const void *base, uint32_t row, uint32_t pitch,
+                                                uint32_t off) {
+    return base ? static_cast<const uint8_t *>(base) + (uint64_t)row * pitch + off : nullptr;
+}
+__device__ __forceinline__ uint8_t *share(void *base, uint32_t row, uint32_t pitch, uint32_t off) {
+    return const_cast<uint8_t *>(share(static_cast<const void *>(base), row, pitch, off));
+}
+
+// Pitches and offsets are 32-bit bytes (one multiply-add to an address): the address arithmetic of
+// a row is a third of its instructions otherwise.
 template <int DT, int NCH, int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS) residual_norm_kernel(const NormArgs a, int tpr_log2) {
     pdl_wait_then_release();
     __shared__ float red[4 * kMaxWarps];
     const int tpr = 1 << tpr_log2;
     const int t = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> tpr_log2) + (threadIdx.x >> tpr_log2);
+    const uint32_t rows = blockDim.x >> tpr_log2;             // of a CTA
+    const uint32_t row = blockIdx.x * rows + (threadIdx.x >> tpr_log2);
     const bool live = row < a.M;
-    const int64_t chunks = a.K / 8;
+    const uint32_t rc = live ? row : 0u;
+    const uint32_t off = t * 16u, step = 16u << tpr_log2;     // this thread's chunks, in bytes
 
-    const uint8_t *xr = static_cast<const uint8_t *>(a.X) + (live ? row : 0) * a.ldx * 2;
-    const uint8_t *rr =
-        a.residual ? static_cast<const uint8_t *>(a.residual) + (live ? row : 0) * a.ldr * 2
-                   : nullptr;
+    const uint8_t *xr = share(a.X, rc, a.x_pitch, off);
+    const uint8_t *rr = share(a.residual, rc, a.r_pitch, off);
     // Rows that CTAs half a wave on will load are fetched into L2 meanwhile, so that HBM works
     // through this wave's sums too (4096 x 12288 layer norm 69.7 -> 66.3 us).  Not beside the MXFP4
     // form, whose extra arithmetic is the bound instead (2048 x 4096: 13.3 -> 14.0 us with it).
     if (t == 0 && !a.codes) {
-        const int64_t next = row + (int64_t)(148 * CTAS / 2) * (blockDim.x >> tpr_log2);
+        const uint32_t next = row + 148 * CTAS / 2 * rows;
         if (next < a.M) {
-            prefetch_l2(static_cast<const uint8_t *>(a.X) + next * a.ldx * 2, a.K * 2);
-            if (rr)
-                prefetch_l2(static_cast<const uint8_t *>(a.residual) + next * a.ldr * 2, a.K * 2);
+            prefetch_l2(share(a.X, next, a.x_pitch, 0), a.pitch);
+            if (rr) prefetch_l2(share(a.residual, next, a.r_pitch, 0), a.pitch);
         }
     }
     Chunk<DT> x[NCH], r[NCH];
     bool in[NCH];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {      // issue every load before using any
-        const int64_t ch = t + ((int64_t)i << tpr_log2);
-        in[i] = live && ch < chunks;
-        x[i] = in[i] ? stream_chunk<DT>(xr, ch) : zero_chunk<DT>();
-        r[i] = in[i] && rr ? stream_chunk<DT>(rr, ch) : zero_chunk<DT>();
+        in[i] = live && off + i * step < a.pitch;
+        x[i] = in[i] ? stream_chunk<DT>(xr + i * step, 0) : zero_chunk<DT>();
+        r[i] = in[i] && rr ? stream_chunk<DT>(rr + i * step, 0) : zero_chunk<DT>();
     }
     float h[NCH][8];
 #pragma unroll
@@ -134,51 +143,52 @@ __global__ void __launch_bounds__(THREADS, CTAS) residual_norm_kernel(const Norm
     float mean, rstd;
     if (a.post_norm != LLMINT8_NORM_NONE) {
         row_norm<NCH>(h, in, a.post_norm, a.inv_k, a.eps, red, tpr, mean, rstd);
+        const uint8_t *w = share(a.post_weight, 0, 0, off), *b = share(a.post_bias, 0, 0, off);
 #pragma unroll
         for (int i = 0; i < NCH; ++i)
             if (in[i])
-                apply_norm<DT>(h[i], a.post_norm, mean, rstd, a.post_weight, a.post_bias,
-                               t + ((int64_t)i << tpr_log2));
+                apply_norm<DT>(h[i], a.post_norm, mean, rstd, w ? w + i * step : nullptr,
+                               b ? b + i * step : nullptr);
     }
-    const uint8_t *gr = a.gate ? static_cast<const uint8_t *>(a.gate) +
-                                     (int64_t)(live ? (uint32_t)row / a.gate_group : 0u) * a.K * 2
-                               : nullptr;
+    const uint8_t *g = a.gate ? share(a.gate, rc / a.gate_group, a.pitch, off) : nullptr;
+    uint8_t *hr = share(a.H, rc, a.pitch, off);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
         if (!in[i]) continue;
-        const int64_t ch = t + ((int64_t)i << tpr_log2);
         float u[8];
-        if (gr) {
-            unpack_chunk<DT>(load_chunk<DT>(gr, ch), u);
+        if (g) {
+            unpack_chunk<DT>(load_chunk<DT>(g + i * step, 0), u);
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] *= u[e];
         }
         unpack_chunk<DT>(r[i], u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[i][e] = fmaf(h[i][e], a.scale, u[e]);
-        if (a.H) store_chunk<DT>(static_cast<uint8_t *>(a.H) + row * a.K * 2, ch,
-                                 pack_chunk<DT>(h[i]));
+        if (hr) store_chunk<DT>(hr + i * step, 0, pack_chunk<DT>(h[i]));
     }
     if (a.norm == LLMINT8_NORM_NONE) return;   // uniform over the grid
     row_norm<NCH>(h, in, a.norm, a.inv_k, a.eps, red + 2 * kMaxWarps, tpr, mean, rstd);
+    const uint8_t *w = share(a.weight, 0, 0, off), *b = share(a.bias, 0, 0, off);
+    uint8_t *yr = share(a.Y, rc, a.pitch, off);
+    uint8_t *cr = share(a.codes, rc, a.pitch / 4, off / 4);
+    // the row's first scale word of this half warp (a warp's 32 chunks are 256 columns)
+    uint8_t *sr = a.scales + ((uint64_t)(row / kMxRows) * a.tiles_k + off / 512) * kMxTile +
+                  (lane >> 4) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-        const int64_t ch = t + ((int64_t)i << tpr_log2);
         Chunk<DT> y = zero_chunk<DT>();
         if (in[i]) {
-            apply_norm<DT>(h[i], a.norm, mean, rstd, a.weight, a.bias, ch);
+            apply_norm<DT>(h[i], a.norm, mean, rstd, w ? w + i * step : nullptr,
+                           b ? b + i * step : nullptr);
             y = pack_chunk<DT>(h[i]);
-            if (a.Y) store_chunk<DT>(static_cast<uint8_t *>(a.Y) + row * a.K * 2, ch, y);
+            if (yr) store_chunk<DT>(yr + i * step, 0, y);
         }
-        // a warp's 32 chunks are one row's share of a scale tile; rows past M pad the last one
-        const int64_t kt = ch >> 5;
-        if (a.codes && row < a.rows_out && kt < a.tiles_k) {
+        // rows past M pad the last row of scale tiles
+        if (cr && row < a.rows_out && (off + i * step) / 512 < a.tiles_k) {
             uint32_t word;
             const uint32_t q = quantize_chunk<DT>(y, word, lane);
-            if (in[i]) reinterpret_cast<uint32_t *>(a.codes)[row * chunks + ch] = q;
-            if ((lane & 15) == 0)
-                *reinterpret_cast<uint32_t *>(
-                    a.scales + scale_word_offset(row, kt, a.tiles_k, lane >> 4)) = word;
+            if (in[i]) *reinterpret_cast<uint32_t *>(cr + i * step / 4) = q;
+            if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(sr + (uint64_t)i * step * 2) = word;
         }
     }
 }
@@ -189,7 +199,7 @@ cudaError_t norm_launch(const NormArgs &a, cudaStream_t s) {
     // idle; of equals, up to 256 threads and then two chunks, since several rows to an SM, in
     // CTAs of their own, keep its memory busy while one of them waits for its sums.  A few rows
     // take one chunk a thread: a lone row's time is its chain of latencies.
-    const int64_t chunks = ceil_div(a.K, kMxCols) * 32;
+    const int64_t chunks = (int64_t)a.tiles_k * 32;
     int best = 10;
     if (a.M <= 148) {
         best = 5;
