@@ -371,7 +371,7 @@ LLMINT8_API size_t llmint8_mxfp4_scales_size(int64_t R, int64_t K);
 
 /*
  * Rows of a matrix (a weight [N, K], or activations [M, K]) to MXFP4.
- *   X       [R, K] of `dtype` (any llmint8_dtype), rows ldx elements apart: K <= ldx <= 2^30 and a
+ *   X       [R, K] of `dtype` (any llmint8_dtype), rows ldx elements apart: K <= ldx < 2^30 and a
  *           row pitch that is a multiple of 16 bytes (else LLMINT8_ERR_INVALID_ARG).
  *   codes, scales  outputs, padding included.
  * Pure function of X: calling it twice gives identical bytes.

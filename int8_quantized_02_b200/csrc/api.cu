@@ -661,9 +661,10 @@ namespace {
 bool mx_k_ok(int64_t K) { return K >= 32 && K % 32 == 0 && K <= 131072; }
 bool mx_rows_ok(int64_t R) { return R >= 0 && R <= (int64_t)INT32_MAX; }
 bool dtype16(int dtype) { return dtype == LLMINT8_F16 || dtype == LLMINT8_BF16; }
-// A row pitch of `ld` elements of `bytes` bytes: K to 2^30 elements, each row on 16 bytes.
+// A row pitch of `ld` elements of `bytes` bytes: at least K, less than 2^30 elements (its bytes are
+// a 32-bit number in the kernels), each row on 16 bytes.
 bool pitch_ok(int64_t ld, int64_t K, int bytes) {
-    return ld >= K && ld <= ((int64_t)1 << 30) && ld * bytes % 16 == 0;
+    return ld >= K && ld < ((int64_t)1 << 30) && ld * bytes % 16 == 0;
 }
 bool mx_pair_ok(const uint8_t *codes, const uint8_t *scales) {
     return codes && scales && aligned16(codes) && aligned16(scales);

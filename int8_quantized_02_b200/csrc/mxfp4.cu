@@ -19,67 +19,73 @@ constexpr int kWarps = kThreads / 32;
 
 constexpr int kRows = 4;                 // rows of a warp, 32 apart
 
-// A warp's tile column and first row.
+// A warp's tile column and first row, and where the scales of its half warp's blocks lie: four
+// words in a row, one for each of its rows.
 struct Place {
-    int64_t row, kt;
+    uint32_t row, kt;
+    __device__ __forceinline__ explicit Place(int wpr_log2) {
+        const uint32_t w = threadIdx.x >> 5;
+        const uint32_t g = blockIdx.x * (kWarps >> wpr_log2) + (w >> wpr_log2);
+        row = (g >> 5) * kMxRows + (g & 31);
+        kt = (blockIdx.y << wpr_log2) + (w & ((1u << wpr_log2) - 1));
+    }
+    __device__ __forceinline__ uint64_t scales(uint32_t tiles_k, int lane) const {
+        return (uint64_t)((row / kMxRows) * tiles_k + kt) * kMxTile + (lane >> 4) * 512 +
+               (row & 31) * 16;
+    }
 };
-__device__ __forceinline__ Place place_of_warp(int wpr_log2) {
-    const int w = threadIdx.x >> 5;
-    const int64_t g = (int64_t)blockIdx.x * (kWarps >> wpr_log2) + (w >> wpr_log2);
-    return Place{(g >> 5) * kMxRows + (g & 31),
-                 ((int64_t)blockIdx.y << wpr_log2) + (w & ((1 << wpr_log2) - 1))};
-}
 
 // Rows R to the next multiple of 128 get zero scales; with `pad` false that is left out for those
 // that no row below R shares a store with.
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
-mxfp4_quantize_kernel(const uint8_t *__restrict__ X, int64_t row_bytes, int64_t R, bool pad,
-                      int64_t chunks, int64_t tiles_k, int wpr_log2,
+mxfp4_quantize_kernel(const uint8_t *__restrict__ X, uint32_t row_bytes, uint32_t R, bool pad,
+                      uint32_t chunks, uint32_t tiles_k, int wpr_log2,
                       uint32_t *__restrict__ codes, uint8_t *__restrict__ scales) {
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31;
-    const Place p = place_of_warp(wpr_log2);
+    const Place p(wpr_log2);
     if (p.kt >= tiles_k || (!pad && p.row >= R)) return;
-    const int64_t ch = p.kt * 32 + lane;
-    const uint8_t *x = X + p.row * row_bytes;
+    const uint32_t ch = p.kt * 32 + lane;
+    const bool in = ch < chunks;
+    const uint8_t *x = X + (uint64_t)p.row * row_bytes + ch * (DT == kF32 ? 32 : 16);
     Chunk<DT> c[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j)      // issue every load before using any
-        c[j] = p.row + 32 * j < R && ch < chunks ? load_chunk<DT>(x + 32 * j * row_bytes, ch)
-                                                 : zero_chunk<DT>();
-    uint32_t *q = codes + p.row * chunks + ch;
+        c[j] = in && p.row + 32 * j < R ? load_chunk<DT>(x + (uint64_t)(32 * j) * row_bytes, 0)
+                                        : zero_chunk<DT>();
+    uint32_t *q = codes + (uint64_t)p.row * chunks + ch;
     uint32_t word[kRows];
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
         const uint32_t v = quantize_chunk<DT>(c[j], word[j], lane);
-        if (p.row + 32 * j < R && ch < chunks) q[32 * j * chunks] = v;
+        if (in && p.row + 32 * j < R) q[(uint64_t)(32 * j) * chunks] = v;
     }
     if ((lane & 15) == 0)
-        *reinterpret_cast<uint4 *>(scales + scale_word_offset(p.row, p.kt, tiles_k, lane >> 4)) =
+        *reinterpret_cast<uint4 *>(scales + p.scales(tiles_k, lane)) =
             make_uint4(word[0], word[1], word[2], word[3]);
 }
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads)
 mxfp4_dequant_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restrict__ scales,
-                     int64_t R, int64_t chunks, int64_t tiles_k, int wpr_log2,
+                     uint32_t R, uint32_t chunks, uint32_t tiles_k, int wpr_log2,
                      uint8_t *__restrict__ out) {
     pdl_wait_then_release();
     const int lane = threadIdx.x & 31;
-    const Place p = place_of_warp(wpr_log2);
-    const int64_t ch = p.kt * 32 + lane;
-    if (ch >= chunks) return;
+    const Place p(wpr_log2);
+    const uint32_t ch = p.kt * 32 + lane;
+    if (ch >= chunks || p.row >= R) return;
     uint32_t q[kRows];
-    const uint32_t *at = codes + p.row * chunks + ch;
+    const uint32_t *at = codes + (uint64_t)p.row * chunks + ch;
 #pragma unroll
     for (int j = 0; j < kRows; ++j)      // issue every load before using any
-        q[j] = p.row + 32 * j < R ? at[32 * j * chunks] : 0u;
-    const uint4 words = *reinterpret_cast<const uint4 *>(
-        scales + scale_word_offset(p.row, p.kt, tiles_k, lane >> 4));
+        q[j] = p.row + 32 * j < R ? at[(uint64_t)(32 * j) * chunks] : 0u;
+    const uint4 words = *reinterpret_cast<const uint4 *>(scales + p.scales(tiles_k, lane));
     const uint32_t word[kRows] = {words.x, words.y, words.z, words.w};
     constexpr int kBytes = DT == kF32 ? 32 : 16;
-    uint8_t *o = out + p.row * chunks * kBytes;
+    const uint32_t pitch = chunks * kBytes;
+    uint8_t *o = out + (uint64_t)p.row * pitch + ch * kBytes;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
         if (p.row + 32 * j >= R) break;
@@ -112,12 +118,11 @@ mxfp4_dequant_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restri
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 g[e] = __shfl_xor_sync(__activemask(), odd ? f[e] : f[4 + e], 1);
-            float4 *pair = reinterpret_cast<float4 *>(o + 32 * j * chunks * kBytes) + (ch & ~1) * 2 +
-                           (lane & 1);
+            float4 *pair = reinterpret_cast<float4 *>(o + (uint64_t)(32 * j) * pitch) - (odd ? 1 : 0);
             pair[0] = odd ? make_float4(g[0], g[1], g[2], g[3]) : make_float4(f[0], f[1], f[2], f[3]);
             pair[2] = odd ? make_float4(f[4], f[5], f[6], f[7]) : make_float4(g[0], g[1], g[2], g[3]);
         } else {
-            store_chunk<DT>(o + 32 * j * chunks * kBytes, ch, pack_chunk<DT>(f));
+            store_chunk<DT>(o + (uint64_t)(32 * j) * pitch, 0, pack_chunk<DT>(f));
         }
     }
 }
@@ -148,7 +153,8 @@ cudaError_t launch_mxfp4_quantize(const void *X, int dtype, int64_t ldx, int64_t
                               : mxfp4_quantize_kernel<kF32>;
     const cudaError_t e =
         launch_pdl(k, sh.grid, dim3(kThreads), s, static_cast<const uint8_t *>(X),
-                   ldx * (dtype == kF32 ? 4 : 2), R, pad, K / 8, tiles_k, sh.wpr_log2,
+                   (uint32_t)(ldx * (dtype == kF32 ? 4 : 2)), (uint32_t)R, pad, (uint32_t)(K / 8),
+                   (uint32_t)tiles_k, sh.wpr_log2,
                    reinterpret_cast<uint32_t *>(codes), scales);
     note_launches(1);
     return e;
@@ -162,8 +168,9 @@ cudaError_t launch_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales, in
              : dtype == kBF16 ? mxfp4_dequant_kernel<kBF16>
                               : mxfp4_dequant_kernel<kF32>;
     const cudaError_t e = launch_pdl(k, sh.grid, dim3(kThreads), s,
-                                     reinterpret_cast<const uint32_t *>(codes), scales, R, K / 8,
-                                     tiles_k, sh.wpr_log2, static_cast<uint8_t *>(out));
+                                     reinterpret_cast<const uint32_t *>(codes), scales, (uint32_t)R,
+                                     (uint32_t)(K / 8), (uint32_t)tiles_k, sh.wpr_log2,
+                                     static_cast<uint8_t *>(out));
     note_launches(1);
     return e;
 }

@@ -171,14 +171,6 @@ __device__ __forceinline__ uint32_t e2m1_codes(const float (&f)[8], float inv) {
     return r;
 }
 
-// Byte offset of the four scales of blocks 4 h .. 4 h + 3 of row `row` in scale tile (row / 128,
-// kt) of a matrix with `tiles_k` tiles to a row of tiles.
-__device__ __forceinline__ int64_t scale_word_offset(int64_t row, int64_t kt, int64_t tiles_k,
-                                                     int h) {
-    const int r = (int)(row & (kMxRows - 1));
-    return ((row / kMxRows) * tiles_k + kt) * kMxTile + h * 512 + (r & 31) * 16 + (r >> 5) * 4;
-}
-
 // Warp-wide: quantises 256 columns of a row whose chunks the lanes hold (zero past K).  Returns
 // this lane's eight codes; `word` gets the scale bytes of its half warp's four blocks.
 template <int DT>

@@ -691,9 +691,10 @@ def _workspace(workspace, dev: torch.device):
     return workspace
 
 
-def _linear_args(X, WC, WS, bias, Y, workspace, s):
-    """(Y, workspace, the C call's arguments) of an MXFP4 layer on raw stream s."""
-    M, K, px, ld = _rows(X, _DTYPES16, "X")
+def _linear_args(rows, X, WC, WS, bias, Y, workspace, s):
+    """(Y, workspace, the C call's arguments) of an MXFP4 layer on raw stream s; `rows` is what
+    _rows says of X."""
+    M, K, px, ld = rows
     dev, dt = X.device, X.dtype
     N, pc, ps = _mxfp4_weight(WC, WS, K, dev)
     pb = _arg(bias, dt, (N,), "bias", dev)
@@ -707,8 +708,10 @@ def llmint8_mxfp4_linear(X: torch.Tensor, WC: torch.Tensor, WS: torch.Tensor, bi
                          workspace=None, stream=None):
     """The MXFP4 layer: Y [M, N] from X [M, K] (fp16 or bf16, quantized in the call) and the weight
     (WC, WS) of llmint8_mxfp4_quantize; bias and Y are of X's type."""
+    rows = _rows(X, _DTYPES16, "X")
+
     def call(s):
-        out, ws, args = _linear_args(X, WC, WS, bias, Y, workspace, s)
+        out, ws, args = _linear_args(rows, X, WC, WS, bias, Y, workspace, s)
         _check(load().llmint8_mxfp4_linear(*args), "llmint8_mxfp4_linear")
         return out
     return _run(X.device, stream, call, X, WC, WS, bias, Y, workspace)
@@ -746,8 +749,9 @@ class Mxfp4LinearPlan:
         self._keep = (X, WC, WS, bias, stream)
         self._device = X.device.index
         self._fn = load().llmint8_mxfp4_linear
+        rows = _rows(X, _DTYPES16, "X")
         self.Y, self.workspace, self._args = _run(
-            X.device, stream, lambda s: _linear_args(X, WC, WS, bias, Y, workspace, s))
+            X.device, stream, lambda s: _linear_args(rows, X, WC, WS, bias, Y, workspace, s))
 
     def __call__(self) -> torch.Tensor:
         if torch.cuda.current_device() == self._device:
