@@ -119,13 +119,13 @@ def assert_product(y, x, w, b, dtype):
     assert (off <= tol).all(), (off / tol).max()
 
 
-SHAPES = [(1, 1, 32), (1, 130, 131072), (3, 200, 8224), (7, 96, 2080), (8, 130, 4096), (8, 257, 16416), (9, 300, 4128), (15, 1000, 2080), (1, 1024, 1024), (2, 130, 64), (5, 129, 96), (16, 512, 4096), (17, 300, 288),
+SHAPES = [(1, 1, 32), (1, 130, 131072), (3, 200, 8224), (7, 96, 2080), (8, 130, 4096), (8, 257, 16416), (9, 300, 4128), (15, 1000, 2080), (16, 77, 16416), (11, 4096, 8192), (1, 1024, 1024), (2, 130, 64), (5, 129, 96), (16, 512, 4096), (17, 300, 288),
           (33, 128, 544), (64, 257, 1056), (65, 96, 2080), (128, 640, 512), (129, 1000, 320),
           (255, 77, 800), (256, 256, 256), (257, 256, 32), (300, 1003, 2080), (513, 520, 96),
           (700, 31, 1312), (1000, 2050, 512), (100, 16000, 96), (1200, 1003, 288),
           (1300, 2500, 1056),
           # enough bands for three CTAs to an SM, and more k-tiles than their stages
-          (2, 38100, 1568), (12, 38100, 1056), (20, 38100, 1056), (50, 38100, 1056)]
+          (2, 38100, 1568), (12, 38100, 1056), (16, 38100, 1568), (20, 38100, 1056), (50, 38100, 1056)]
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16])
