@@ -703,8 +703,7 @@ llmint8_status check_mxfp4(int dtype, int64_t M, int64_t K, const uint8_t *Wc, c
 // The product between the process-wide profile events (when set).
 llmint8_status run_mxfp4(const void *X, int64_t ldx, const uint8_t *Xc, const uint8_t *Xs,
                          int64_t M, int64_t K, const uint8_t *Wc, const uint8_t *Ws, int64_t N,
-                         const void *bias, void *Y, int dtype, int weights_ready, void *ws,
-                         cudaStream_t s) {
+                         const void *bias, void *Y, int dtype, void *ws, cudaStream_t s) {
     Mxfp4Gemm g;
     g.X = X;
     g.ldx = ldx;
@@ -715,18 +714,13 @@ llmint8_status run_mxfp4(const void *X, int64_t ldx, const uint8_t *Xc, const ui
     g.bias = bias;
     g.Y = Y;
     g.dtype = dtype;
-    g.weights_ready = weights_ready;
     g.status = next_status(at<WsHeader>(ws, 0));
     g.M = M;
     g.N = N;
     g.K = K;
     g.timeout_ns = g_timeout_ns.load();
     cudaEvent_t ev0 = g_prof_start.load(), ev1 = g_prof_stop.load();
-    if (ev0) {
-        // the event's record stands between the quantisation and the product
-        g.weights_ready = 0;
-        if (record_profile_event(ev0, s) != cudaSuccess) return LLMINT8_ERR_CUDA;
-    }
+    if (ev0 && record_profile_event(ev0, s) != cudaSuccess) return LLMINT8_ERR_CUDA;
     if (launch_mxfp4_gemm(g, s) != cudaSuccess) return LLMINT8_ERR_CUDA;
     if (ev1 && record_profile_event(ev1, s) != cudaSuccess) return LLMINT8_ERR_CUDA;
     return LLMINT8_OK;
@@ -782,14 +776,14 @@ llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t
     if (!X || !aligned16(X) || !pitch_ok(ldx, K, 2)) return LLMINT8_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M <= kMxfp4FusedRows)
-        return run_mxfp4(X, ldx, nullptr, nullptr, M, K, Wc, Ws, N, bias, Y, dtype, 0, ws, s);
+        return run_mxfp4(X, ldx, nullptr, nullptr, M, K, Wc, Ws, N, bias, Y, dtype, ws, s);
     const Mxfp4Layout L = mxfp4_layout(M, K);
     uint8_t *Xc = at<uint8_t>(ws, L.codes), *Xs = at<uint8_t>(ws, L.scales);
     // rows past M of the last scale tile meet only codes that read as zero, in columns of the
     // product that are not stored: they stay as they are
     if (launch_mxfp4_quantize(X, dtype, ldx, M, false, K, Xc, Xs, s) != cudaSuccess)
         return LLMINT8_ERR_CUDA;
-    return run_mxfp4(nullptr, 0, Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 1, ws, s);
+    return run_mxfp4(nullptr, 0, Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, ws, s);
 }
 
 llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, const uint8_t *Xs, int64_t M,
@@ -802,7 +796,7 @@ llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, const uint8_t *
     if (chk != LLMINT8_OK) return chk;
     if (M == 0) return LLMINT8_OK;
     if (!mx_pair_ok(Xc, Xs)) return LLMINT8_ERR_INVALID_ARG;
-    return run_mxfp4(nullptr, 0, Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, 0, ws,
+    return run_mxfp4(nullptr, 0, Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, ws,
                      static_cast<cudaStream_t>(stream));
 }
 

@@ -498,7 +498,6 @@ struct BArgs {
     int tiles_k, last_mma;
     int splits;                          // CTAs of a cluster
     int stages;
-    int weights_ready;                   // the weight may be read before griddepcontrol.wait
     uint64_t timeout_ns;
 };
 
@@ -557,19 +556,14 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const BoundedWait wait{&tail->abort_flag, a.status, a.timeout_ns};
     LLMINT8_DCHECK((smem_addr(smem) & 1023u) == 0, a.status);
 
-    auto load_w = [&](int it, int stage) {
+    const auto load = [&](int it, int stage) {
         const uint32_t full = smem_addr(&tail->full[stage]);
         const uint32_t sa = smem_addr(smem + stage * C::STAGE);
         const int kt = k_begin + it;
         mbar_arrive_expect_tx(full, FUSED ? ROWS * KB + kMxTile : C::STAGE);
         tma_load_2d(sa, &tmW, kt * KB, band * ROWS, full);
         tma_load_2d(sa + (ROWS + NT) * KB, &tmWS, 0, band * a.tiles_k + kt, full);
-    };
-    auto load_x = [&](int it, int stage) {
         if (FUSED) return;
-        const uint32_t full = smem_addr(&tail->full[stage]);
-        const uint32_t sa = smem_addr(smem + stage * C::STAGE);
-        const int kt = k_begin + it;
         tma_load_2d(sa + ROWS * KB, &tmX, kt * KB, m0, full);
         // scale tiles past the last row of tiles read as zero
 #pragma unroll
@@ -580,25 +574,18 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 
     if (warp == 0) {
         if (elect_one()) {
-            // Right behind the quantisation of X in one call, the weight does not depend on the
-            // kernel that is still running: its first stages are on their way meanwhile.
-            // Elsewhere that kernel may be writing it: then L2, where every write lands, is asked to
-            // fetch them.
-            const int first = min(stages, k_count);
-            const int pre = a.weights_ready ? first : 0;
-            for (int it = 0; it < pre; ++it) load_w(it, it);
-            for (int it = pre; it < first; ++it) {
+            // The kernel that is still running may be writing the weight: L2, where every write lands,
+            // is asked to fetch the first stages of it meanwhile.
+            for (int it = 0; it < min(stages, k_count); ++it) {
                 tma_prefetch_l2_2d(&tmW, (k_begin + it) * KB, band * ROWS);
                 tma_prefetch_l2_2d(&tmWS, 0, band * a.tiles_k + k_begin + it);
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            for (int it = 0; it < pre; ++it) load_x(it, it);
-            int it = pre, stage = pre % stages;
-            uint32_t phase = (uint32_t)(pre / stages);
+            int it = 0, stage = 0;
+            uint32_t phase = 0;
             for (; it < k_count; ++it) {
                 if (!wait(smem_addr(&tail->empty[stage]), phase ^ 1)) break;
-                load_w(it, stage);
-                load_x(it, stage);
+                load(it, stage);
                 if (++stage == stages) {
                     stage = 0;
                     phase ^= 1;
@@ -849,7 +836,6 @@ cudaError_t band(const Mxfp4Gemm &g, int tiles_k, int last_mma, int sms, cudaStr
     a.N = (int)g.N;
     a.tiles_k = tiles_k;
     a.last_mma = last_mma;
-    a.weights_ready = g.weights_ready;
     a.timeout_ns = g.timeout_ns;
     a.splits = band_splits(tiles, tiles_k, sms);
     a.stages = tiles * a.splits > 2 * sms ? Band<NT>::FEW : Band<NT>::STAGES;

@@ -166,7 +166,6 @@ struct Mxfp4Gemm {
     const void *bias;        // [N] or null
     void *Y;                 // [M, N]
     int dtype;               // of bias and Y
-    int weights_ready;       // W does not depend on the kernel launched last on the stream
     StatusRef status;
     int64_t M, N, K;
     uint64_t timeout_ns;

@@ -42,7 +42,9 @@ __global__ void __launch_bounds__(kThreads)
 mxfp4_quantize_kernel(const uint8_t *__restrict__ X, uint32_t row_bytes, uint32_t R, bool pad,
                       uint32_t chunks, uint32_t tiles_k, int wpr_log2,
                       uint32_t *__restrict__ codes, uint8_t *__restrict__ scales) {
-    pdl_wait_then_release();
+    // a product that follows sets up, and asks L2 for its weight, while this waits and works
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31;
     const Place p(wpr_log2);
     if (p.kt >= tiles_k || (!pad && p.row >= R)) return;
