@@ -287,8 +287,8 @@ LLMINT8_API llmint8_status llmint8_set_wait_timeout_ns(uint64_t ns);
  * Measurement hooks (no counterpart on the pages; they let a benchmark time the product
  * kernel of a call with CUDA events and count launches):
  *   llmint8_set_profile_events(start, stop): two cudaEvent_t.  While both are non-NULL,
- *     every llmint8_linear, llmint8_linear_next_bitmaps, llmint8_linear_with_bitmaps and
- *     llmint8_linear_noalloc call records `start` on its stream immediately before its
+ *     every llmint8_linear, llmint8_linear_next_bitmaps, llmint8_linear_with_bitmaps,
+ *     llmint8_linear_noalloc, llmint8_mxfp4_linear and llmint8_mxfp4_linear_quantized call records `start` on its stream immediately before its
  *     product kernel (the GEMM; on the decode path, the decode kernel) and `stop`
  *     immediately after it.  NULL, NULL disables.
  *     Process-wide; the caller owns the events and must keep them alive while set.
@@ -396,9 +396,13 @@ LLMINT8_API llmint8_status llmint8_mxfp4_dequant(const uint8_t *codes, const uin
  *   ws      device workspace of llmint8_mxfp4_linear_workspace_size(M, N, K) bytes; its device
  *           status is read with llmint8_device_status().  Calls that may overlap need a workspace
  *           each; calls in stream order may share one.
+ * Y must not overlap the other arguments.
  * Kernels: few rows of X stream the weight as the MMA's 128-row operand, k split over the CTAs of
- * a cluster; more run CTA pairs on 256 x 256 tiles.  Results do not depend on timing; the
- * same rows in calls of different M may differ in the last fp32 rounding of a sum.
+ * a cluster, and up to 8 rows are quantised in that kernel; more rows run a launch that quantises
+ * them and, when they are many, CTA pairs on 256 x 256 tiles.  Results do not depend on timing; the
+ * same rows in calls of different M may differ in the last fp32 rounding of a sum.  The kernels of
+ * these calls are programmatic dependents, as llmint8_linear's; they let the next kernel of the
+ * stream set up while they run.
  */
 LLMINT8_API llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t K,
                                     int64_t ldx, const uint8_t *Wc, const uint8_t *Ws, int64_t N,

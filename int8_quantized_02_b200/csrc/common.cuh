@@ -48,7 +48,7 @@ __device__ __forceinline__ void pdl_wait_then_release() {
 // True in one thread of a converged warp.  The tensor-core and TMA instructions take their
 // operands in uniform registers; behind this the compiler knows that one thread is active and
 // moves them there directly, where a branch on the lane makes it search for the active lanes each
-// time (MMA issue: 125 clocks against 65 measured).
+// time (measured: 125 clocks to issue an MMA against 39, 108 for a scale copy against 8).
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile(

@@ -5,7 +5,7 @@
 // r + 64 and r + 96 of a scale tile, all of whose loads are in flight at once.  A block's maximum
 // is two shuffles among four lanes, its codes one 32-bit store a lane; and the scales of those
 // four rows are neighbours in the tile, so that half a warp's four blocks of each row make one
-// 16-byte store.  (With one row to a warp and 4-byte stores: 38 us for [16384, 4096] fp16.)
+// 16-byte store.  16384 x 4096 fp16: 30 us, 5.7 TB/s (with one row to a warp and 4-byte stores 38 us).
 #include "kernels.h"
 #include "launch.cuh"
 #include "mxfp4.cuh"
