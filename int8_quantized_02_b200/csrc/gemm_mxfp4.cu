@@ -529,6 +529,13 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     // this CTA's k-tiles
     const int k_begin = (int)((int64_t)a.tiles_k * rank / S);
     const int k_count = (int)((int64_t)a.tiles_k * (rank + 1) / S) - k_begin;
+    // ... from a place that depends on the band, so that the CTAs do not all read the same part of X, nor
+    // the same columns of the weight, at one time (16 x 16384 x 4096: 11.4 us without, 10.7 with)
+    const int k_first = first_kblock(band, k_count);
+    const auto ktile = [&](int it) {
+        const int k = k_first + it;
+        return k_begin + (k >= k_count ? k - k_count : k);
+    };
 
     // the next kernel may set up, and ask L2 for its weight, while this one runs
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -559,7 +566,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const auto load = [&](int it, int stage) {
         const uint32_t full = smem_addr(&tail->full[stage]);
         const uint32_t sa = smem_addr(smem + stage * C::STAGE);
-        const int kt = k_begin + it;
+        const int kt = ktile(it);
         mbar_arrive_expect_tx(full, FUSED ? ROWS * KB + kMxTile : C::STAGE);
         tma_load_2d(sa, &tmW, kt * KB, band * ROWS, full);
         tma_load_2d(sa + (ROWS + NT) * KB, &tmWS, 0, band * a.tiles_k + kt, full);
@@ -577,8 +584,8 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             // The kernel that is still running may be writing the weight: L2, where every write lands,
             // is asked to fetch the first stages of it meanwhile.
             for (int it = 0; it < min(stages, k_count); ++it) {
-                tma_prefetch_l2_2d(&tmW, (k_begin + it) * KB, band * ROWS);
-                tma_prefetch_l2_2d(&tmWS, 0, band * a.tiles_k + k_begin + it);
+                tma_prefetch_l2_2d(&tmW, ktile(it) * KB, band * ROWS);
+                tma_prefetch_l2_2d(&tmWS, 0, band * a.tiles_k + ktile(it));
             }
             asm volatile("griddepcontrol.wait;" ::: "memory");
             int it = 0, stage = 0;
@@ -609,7 +616,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 const uint32_t ss = sa + (ROWS + NT) * KB;
                 mma_ktile<false, ROWS, NT>(tmem, sa, sa + ROWS * KB, ss, ss + kMxTile,
                                            tmem + C::SF, (uint32_t)(m0 & (kMxRows - 1)) >> 5,
-                                           k_begin + it == a.tiles_k - 1 ? a.last_mma : 4,
+                                           ktile(it) == a.tiles_k - 1 ? a.last_mma : 4,
                                            it == 0);
                 tc_commit(smem_addr(&tail->empty[stage]));
                 if (++stage == stages) {
@@ -629,7 +636,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         if (FUSED && warp >= 2 && warp - 2 < turns) {
             for (int it = warp - 2; it < k_count; it += turns) {
                 const int stage = it % stages;
-                const int64_t kt = k_begin + it, ch = kt * 32 + lane;
+                const int64_t ch = (int64_t)ktile(it) * 32 + lane;
                 Chunk<DT> c[kMxfp4FusedRows];
 #pragma unroll
                 for (int m = 0; m < kMxfp4FusedRows; ++m)
