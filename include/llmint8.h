@@ -373,14 +373,15 @@ LLMINT8_API size_t llmint8_mxfp4_scales_size(int64_t R, int64_t K);
  * Rows of a matrix (a weight [N, K], or activations [M, K]) to MXFP4.
  *   X       [R, K] of `dtype` (any llmint8_dtype), rows ldx elements apart: K <= ldx < 2^30 and a
  *           row pitch that is a multiple of 16 bytes (else LLMINT8_ERR_INVALID_ARG).
- *   codes, scales  outputs, padding included.
+ *   codes, scales  outputs, padding included; they must not overlap X or one another.
  * Pure function of X: calling it twice gives identical bytes.
  */
 LLMINT8_API llmint8_status llmint8_mxfp4_quantize(const void *X, int dtype, int64_t R, int64_t K,
                                       int64_t ldx, uint8_t *codes, uint8_t *scales,
                                       void *stream);
 
-/* MXFP4 to values: out [R, K] of `dtype` (any llmint8_dtype), code * scale rounded once. */
+/* MXFP4 to values: out [R, K] of `dtype` (any llmint8_dtype), code * scale rounded once; out must not
+ * overlap the codes or scales. */
 LLMINT8_API llmint8_status llmint8_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales,
                                      int64_t R, int64_t K, void *out, int dtype, void *stream);
 
@@ -396,7 +397,7 @@ LLMINT8_API llmint8_status llmint8_mxfp4_dequant(const uint8_t *codes, const uin
  *   ws      device workspace of llmint8_mxfp4_linear_workspace_size(M, N, K) bytes; its device
  *           status is read with llmint8_device_status().  Calls that may overlap need a workspace
  *           each; calls in stream order may share one.
- * Y must not overlap the other arguments.
+ * Y and ws must not overlap the other arguments (LLMINT8_ERR_INVALID_ARG).
  * Kernels: few rows of X stream the weight as the MMA's 128-row operand, k split over the CTAs of
  * a cluster, and up to 8 rows are quantised in that kernel; more rows run a launch that quantises
  * them and, when they are many, CTA pairs on 256 x 256 tiles.  Results do not depend on timing; the
@@ -441,8 +442,8 @@ LLMINT8_API llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, con
  *   norm       LLMINT8_NORM_NONE leaves y out (Y, codes and scales must then be NULL).  weight,
  *              bias: [K] or NULL.
  *   eps        >= 0, for both norms.
- *   H          [M, K] output, or NULL.  May be the residual's or X's own (dense) buffer.
- *   Y          [M, K] output, or NULL.  May be X's own buffer.
+ *   H, Y       [M, K] outputs, or NULL.  Each may be X's or the residual's own (dense) buffer, but not
+ *              both the same; any other overlap of an output is refused.
  *   codes, scales  MXFP4 form of y (both or neither NULL), padding included.
  * At least one output is given.  K <= 32768 here (a row lives in one CTA's registers); every
  * pointer is 16-byte aligned; all vectors are of `dtype`.

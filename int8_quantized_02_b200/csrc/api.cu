@@ -7,6 +7,7 @@
 
 #include <atomic>
 #include <chrono>
+#include <initializer_list>
 #include <mutex>
 
 #include <nvtx3/nvToolsExt.h>
@@ -670,6 +671,31 @@ bool mx_pair_ok(const uint8_t *codes, const uint8_t *scales) {
     return codes && scales && aligned16(codes) && aligned16(scales);
 }
 
+// Memory of an argument: [at, at + bytes).
+struct Span {
+    const void *at;
+    int64_t bytes;
+};
+bool overlap(Span a, Span b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+    return a.at && b.at && a.bytes > 0 && b.bytes > 0 && x < y + (uintptr_t)b.bytes &&
+           y < x + (uintptr_t)a.bytes;
+}
+// Whether an output shares memory with an input or with another output: its kernels read and write
+// in no fixed order, so such a call has no defined result.
+bool any_overlap(std::initializer_list<Span> outputs, std::initializer_list<Span> inputs) {
+    for (const Span *o = outputs.begin(); o != outputs.end(); ++o) {
+        for (const Span &i : inputs)
+            if (overlap(*o, i)) return true;
+        for (const Span *p = o + 1; p != outputs.end(); ++p)
+            if (overlap(*o, *p)) return true;
+    }
+    return false;
+}
+Span rows_span(const void *p, int64_t rows, int64_t ld, int64_t K, int bytes) {
+    return Span{p, ((rows - 1) * ld + K) * bytes};
+}
+
 size_t mx_scales_bytes(int64_t R, int64_t K) {
     return (size_t)(ceil_div(R, 128) * ceil_div(K, 256) * 1024);
 }
@@ -697,7 +723,11 @@ llmint8_status check_mxfp4(int dtype, int64_t M, int64_t K, const uint8_t *Wc, c
     if (!mx_pair_ok(Wc, Ws) || !Y || !ws || !aligned16(Y) || !aligned16(ws) ||
         (bias && !aligned16(bias)))
         return LLMINT8_ERR_INVALID_ARG;
-    return ws_bytes < need ? LLMINT8_ERR_WORKSPACE_TOO_SMALL : LLMINT8_OK;
+    if (ws_bytes < need) return LLMINT8_ERR_WORKSPACE_TOO_SMALL;
+    return any_overlap({{Y, M * N * 2}, {ws, (int64_t)need}},
+                       {{Wc, N * (K / 2)}, {Ws, (int64_t)mx_scales_bytes(N, K)}, {bias, N * 2}})
+               ? LLMINT8_ERR_INVALID_ARG
+               : LLMINT8_OK;
 }
 
 // The product between the process-wide profile events (when set).
@@ -748,6 +778,9 @@ llmint8_status llmint8_mxfp4_quantize(const void *X, int dtype, int64_t R, int64
     if (!X || !aligned16(X) || !mx_pair_ok(codes, scales) ||
         !pitch_ok(ldx, K, dtype == LLMINT8_F32 ? 4 : 2))
         return LLMINT8_ERR_INVALID_ARG;
+    if (any_overlap({{codes, R * (K / 2)}, {scales, (int64_t)mx_scales_bytes(R, K)}},
+                    {rows_span(X, R, ldx, K, dtype == LLMINT8_F32 ? 4 : 2)}))
+        return LLMINT8_ERR_INVALID_ARG;
     return from_cuda(launch_mxfp4_quantize(X, dtype, ldx, R, true, K, codes, scales,
                                            static_cast<cudaStream_t>(stream)));
 }
@@ -759,6 +792,9 @@ llmint8_status llmint8_mxfp4_dequant(const uint8_t *codes, const uint8_t *scales
     if (!mx_rows_ok(R) || !mx_k_ok(K)) return LLMINT8_ERR_UNSUPPORTED_SHAPE;
     if (R == 0) return LLMINT8_OK;
     if (!mx_pair_ok(codes, scales) || !out || !aligned16(out)) return LLMINT8_ERR_INVALID_ARG;
+    if (any_overlap({{out, R * K * (dtype == LLMINT8_F32 ? 4 : 2)}},
+                    {{codes, R * (K / 2)}, {scales, (int64_t)mx_scales_bytes(R, K)}}))
+        return LLMINT8_ERR_INVALID_ARG;
     return from_cuda(launch_mxfp4_dequant(codes, scales, R, K, out, dtype,
                                           static_cast<cudaStream_t>(stream)));
 }
@@ -773,7 +809,9 @@ llmint8_status llmint8_mxfp4_linear(const void *X, int dtype, int64_t M, int64_t
         check_mxfp4(dtype, M, K, Wc, Ws, N, bias, Y, ws, ws_bytes, need);
     if (chk != LLMINT8_OK) return chk;
     if (M == 0) return LLMINT8_OK;
-    if (!X || !aligned16(X) || !pitch_ok(ldx, K, 2)) return LLMINT8_ERR_INVALID_ARG;
+    if (!X || !aligned16(X) || !pitch_ok(ldx, K, 2) ||
+        any_overlap({{Y, M * N * 2}, {ws, (int64_t)need}}, {rows_span(X, M, ldx, K, 2)}))
+        return LLMINT8_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (M <= kMxfp4FusedRows)
         return run_mxfp4(X, ldx, nullptr, nullptr, M, K, Wc, Ws, N, bias, Y, dtype, ws, s);
@@ -795,7 +833,10 @@ llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, const uint8_t *
         check_mxfp4(dtype, M, K, Wc, Ws, N, bias, Y, ws, ws_bytes, sizeof(WsHeader));
     if (chk != LLMINT8_OK) return chk;
     if (M == 0) return LLMINT8_OK;
-    if (!mx_pair_ok(Xc, Xs)) return LLMINT8_ERR_INVALID_ARG;
+    if (!mx_pair_ok(Xc, Xs) ||
+        any_overlap({{Y, M * N * 2}, {ws, (int64_t)sizeof(WsHeader)}},
+                    {{Xc, M * (K / 2)}, {Xs, (int64_t)mx_scales_bytes(M, K)}}))
+        return LLMINT8_ERR_INVALID_ARG;
     return run_mxfp4(nullptr, 0, Xc, Xs, M, K, Wc, Ws, N, bias, Y, dtype, ws,
                      static_cast<cudaStream_t>(stream));
 }
@@ -824,6 +865,19 @@ llmint8_status llmint8_residual_norm(const void *X, int dtype, int64_t M, int64_
     if (post_norm == LLMINT8_NORM_NONE && (post_weight || post_bias)) return LLMINT8_ERR_INVALID_ARG;
     if (!H && !Y && !codes) return LLMINT8_ERR_INVALID_ARG;
     if (gate && (gate_rows < 1 || M % gate_rows != 0)) return LLMINT8_ERR_INVALID_ARG;
+    // H and Y may each be X's or the residual's own dense buffer: a thread reads its part of a row
+    // before it writes there.  Otherwise nothing that is written overlaps anything.
+    const int64_t dense = M * K * 2, vec = K * 2;
+    const Span x = rows_span(X, M, ldx, K, 2), r = rows_span(residual, M, ldr, K, 2), h = {H, dense},
+               y = {Y, dense}, c = {codes, M * (K / 2)}, s = {scales, (int64_t)mx_scales_bytes(M, K)};
+    const auto own = [&](Span o, Span in, int64_t ld) {
+        return !overlap(o, in) || (o.at == in.at && (ld == K || M == 1));
+    };
+    if (!own(h, x, ldx) || !own(h, r, ldr) || !own(y, x, ldx) || !own(y, r, ldr) ||
+        any_overlap({h, y, c, s}, {{post_weight, vec}, {post_bias, vec}, {weight, vec}, {bias, vec},
+                                   {gate, gate ? gate_rows * vec : 0}}) ||
+        any_overlap({c, s}, {x, r}))
+        return LLMINT8_ERR_INVALID_ARG;
     NormArgs a;
     a.X = X;
     a.residual = residual;

@@ -112,6 +112,37 @@ def test_linear_refusals(lib):
     assert quantized(xc=None) == quantized(xs=ODD) == L.ERR_INVALID_ARG
 
 
+def test_outputs_that_overlap_are_refused(lib):
+    at = lambda off: ctypes.c_void_p((1 << 20) + off)  # noqa: E731
+    far = ctypes.c_void_p(1 << 30)
+    bad = L.ERR_INVALID_ARG
+    q = lib.llmint8_mxfp4_quantize
+    assert q(at(0), 0, 4, 64, 64, at(496), far, None) == bad       # codes in X's last row
+    assert q(at(0), 0, 4, 64, 64, far, at(0), None) == bad
+    assert q(at(0), 0, 4, 64, 64, far, far, None) == bad
+    d = lib.llmint8_mxfp4_dequant
+    assert d(at(0), far, 4, 64, at(112), 0, None) == bad
+    assert d(far, at(0), 4, 64, at(1008), 0, None) == bad
+
+    def linear(x=at(0), wc=at(1 << 16), ws=at(2 << 16), y=at(3 << 16), b=None, w=at(4 << 16)):
+        return lib.llmint8_mxfp4_linear(x, 0, 4, 64, 64, wc, ws, 8, b, y, w, 4096, None)
+    assert linear(y=at(496)) == linear(y=at((1 << 16) + 240)) == linear(y=at((2 << 16) + 1008)) == bad
+    assert linear(b=at((3 << 16) + 48)) == linear(w=at((3 << 16) + 48)) == linear(w=at(0)) == bad
+    f = lib.llmint8_mxfp4_linear_quantized
+    assert f(at(0), far, 4, 64, at(1 << 16), at(2 << 16), 8, None, at(112), 0, at(4 << 16), 256,
+             None) == bad
+
+    def norm(H=at(1 << 16), Y=at(2 << 16), c=None, s=None, ldx=64, w=None):
+        return lib.llmint8_residual_norm(at(0), 0, 4, 64, ldx, at(3 << 16), 64, 0, None, None, None,
+                                         1, ctypes.c_float(1), 1, w, None, ctypes.c_float(0), H, Y,
+                                         c, s, None)
+    assert norm(H=at(16)) == norm(Y=at((3 << 16) + 16)) == bad     # shifted against X, the residual
+    assert norm(H=at(0), ldx=72) == bad                            # X's buffer, but not X's rows
+    assert norm(H=at(1 << 16), Y=at(1 << 16)) == norm(H=at(0), Y=at(0)) == bad
+    assert norm(c=at(0), s=far) == norm(c=far, s=at((3 << 16) + 496)) == bad
+    assert norm(w=at((2 << 16) + 496)) == bad
+
+
 def test_residual_norm_refusals(lib):
     nan, inf = float("nan"), float("inf")
 
