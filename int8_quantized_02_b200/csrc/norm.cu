@@ -106,7 +106,9 @@ __device__ __forceinline__ uint8_t *share(void *base, uint32_t row, uint32_t pit
 // Pitches and offsets are 32-bit bytes, one multiply-add to an address (with 64-bit ones a tenth more
 // instructions, which is what bounds the fuller forms: 75 against 71 us for 4096 x 12288 with norms on
 // both sides and a gate, 89 against 82 to MXFP4).
-template <int DT, int NCH, int THREADS, int CTAS>
+// FULL: the row fills its threads' chunks (as K = 1024, 4096 or 12288 does), which leaves out the
+// tests of each of them, a tenth of the instructions again (71 against 65 us, 82 against 77).
+template <int DT, int NCH, int THREADS, int CTAS, bool FULL>
 __global__ void __launch_bounds__(THREADS, CTAS) residual_norm_kernel(const NormArgs a, int tpr_log2) {
     pdl_wait_then_release();
     __shared__ float red[4 * kMaxWarps];
@@ -134,7 +136,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) residual_norm_kernel(const Norm
     bool in[NCH];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {      // issue every load before using any
-        in[i] = live && off + i * step < a.pitch;
+        in[i] = FULL || off + i * step < a.pitch;
         x[i] = in[i] ? stream_chunk<DT>(xr + i * step, 0) : zero_chunk<DT>();
         r[i] = in[i] && rr ? stream_chunk<DT>(rr + i * step, 0) : zero_chunk<DT>();
     }
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(THREADS, CTAS) residual_norm_kernel(const Norm
         unpack_chunk<DT>(r[i], u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[i][e] = fmaf(h[i][e], a.scale, u[e]);
-        if (hr) store_chunk<DT>(hr + i * step, 0, pack_chunk<DT>(h[i]));
+        if (hr && live) store_chunk<DT>(hr + i * step, 0, pack_chunk<DT>(h[i]));
     }
     if (a.norm == LLMINT8_NORM_NONE) return;   // uniform over the grid
     row_norm<NCH>(h, in, a.norm, a.inv_k, a.eps, red + 2 * kMaxWarps, tpr, mean, rstd);
@@ -182,13 +184,14 @@ __global__ void __launch_bounds__(THREADS, CTAS) residual_norm_kernel(const Norm
             apply_norm<DT>(h[i], a.norm, mean, rstd, w ? w + i * step : nullptr,
                            b ? b + i * step : nullptr);
             y = pack_chunk<DT>(h[i]);
-            if (yr) store_chunk<DT>(yr + i * step, 0, y);
+            if (yr && live) store_chunk<DT>(yr + i * step, 0, y);
         }
-        // rows past M pad the last row of scale tiles
+        // rows past M pad the last row of scale tiles with those of zeros
+        if (!live) y = zero_chunk<DT>();
         if (cr && row < a.rows_out && (off + i * step) / 512 < a.tiles_k) {
             uint32_t word;
             const uint32_t q = quantize_chunk<DT>(y, word, lane);
-            if (in[i]) *reinterpret_cast<uint32_t *>(cr + i * step / 4) = q;
+            if (in[i] && live) *reinterpret_cast<uint32_t *>(cr + i * step / 4) = q;
             if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(sr + (uint64_t)i * step * 2) = word;
         }
     }
@@ -221,20 +224,28 @@ cudaError_t norm_launch(const NormArgs &a, cudaStream_t s) {
     const int threads = std::max(1 << best, 256);
     const int64_t rows = a.codes ? a.rows_out : a.M;
     const dim3 grid((unsigned)ceil_div(rows, threads >> best));
-    const auto go = [&](auto kernel) { return launch_pdl(kernel, grid, dim3(threads), s, a, best); };
-    if (threads == 256) {
-        if (per == 1) return go(residual_norm_kernel<DT, 1, 256, 8>);
-        if (per == 2) return go(residual_norm_kernel<DT, 2, 256, 6>);
-        return per == 3 ? go(residual_norm_kernel<DT, 3, 256, 4>)
-                        : go(residual_norm_kernel<DT, 4, 256, 4>);
-    }
+    const bool full = a.pitch == (uint32_t)per * (16u << best);
+    const auto go = [&](auto when_full, auto otherwise) {
+        return launch_pdl(full ? when_full : otherwise, grid, dim3(threads), s, a, best);
+    };
+#define LLMINT8_NORM(N, THREADS, CTAS)                     \
+    go(residual_norm_kernel<DT, N, THREADS, CTAS, true>, \
+       residual_norm_kernel<DT, N, THREADS, CTAS, false>)
+    if (threads == 256)
+        return per == 1   ? LLMINT8_NORM(1, 256, 8)
+               : per == 2 ? LLMINT8_NORM(2, 256, 6)
+               : per == 3 ? LLMINT8_NORM(3, 256, 4)
+                          : LLMINT8_NORM(4, 256, 4);
     if (threads == 512)
-        return per == 1 ? go(residual_norm_kernel<DT, 1, 512, 2>)
-                        : per <= 3 ? go(residual_norm_kernel<DT, 3, 512, 2>)
-                                   : go(residual_norm_kernel<DT, 4, 512, 2>);
-    return per == 1 ? go(residual_norm_kernel<DT, 1, 1024, 1>)
-                    : per == 2 ? go(residual_norm_kernel<DT, 2, 1024, 1>)
-                               : go(residual_norm_kernel<DT, 4, 1024, 1>);
+        return per == 1   ? LLMINT8_NORM(1, 512, 2)
+               : per == 2 ? LLMINT8_NORM(2, 512, 2)
+               : per == 3 ? LLMINT8_NORM(3, 512, 2)
+                          : LLMINT8_NORM(4, 512, 2);
+    return per == 1   ? LLMINT8_NORM(1, 1024, 1)
+           : per == 2 ? LLMINT8_NORM(2, 1024, 1)
+           : per == 3 ? LLMINT8_NORM(3, 1024, 1)
+                      : LLMINT8_NORM(4, 1024, 1);
+#undef LLMINT8_NORM
 }
 
 }  // namespace
