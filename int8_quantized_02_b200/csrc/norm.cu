@@ -200,9 +200,10 @@ __global__ void __launch_bounds__(THREADS, CTAS) residual_norm_kernel(const Norm
 template <int DT>
 cudaError_t norm_launch(const NormArgs &a, cudaStream_t s) {
     // Threads to a row (a power of two) and chunks to a thread (at most 4): what leaves the fewest
-    // idle; of equals, up to 256 threads and then two chunks, since several rows to an SM, in
-    // CTAs of their own, keep its memory busy while one of them waits for its sums.  A few rows
-    // take one chunk a thread: a lone row's time is its chain of latencies.
+    // idle; of equals, up to 256 threads, else up to 512, and then two chunks, since several rows
+    // to an SM, in CTAs of their own, keep its memory busy while one of them waits for its sums
+    // (4096 x 16384 layer norm: 84 us with 512 threads, 99 with 1024).  A few rows take one chunk a
+    // thread: a lone row's time is its chain of latencies.
     const int64_t chunks = (int64_t)a.tiles_k * 32;
     int best = 10;
     if (a.M <= 148) {
@@ -213,7 +214,7 @@ cudaError_t norm_launch(const NormArgs &a, cudaStream_t s) {
         for (int l = 5; l <= 10; ++l) {
             const int64_t n = ceil_div(chunks, (int64_t)1 << l);
             if (n > 4) continue;
-            const int64_t cost = ((n << l) << 4) + (l > 8 ? 4 : 0) + (n == 1 ? 2 : 0) + n;
+            const int64_t cost = ((n << l) << 4) + (l > 9 ? 8 : l > 8 ? 4 : 0) + (n == 1 ? 2 : 0) + n;
             if (cost < least) {
                 least = cost;
                 best = l;
@@ -238,9 +239,8 @@ cudaError_t norm_launch(const NormArgs &a, cudaStream_t s) {
                           : LLMINT8_NORM(4, 256, 4);
     if (threads == 512)
         return per == 1   ? LLMINT8_NORM(1, 512, 2)
-               : per == 2 ? LLMINT8_NORM(2, 512, 2)
                : per == 3 ? LLMINT8_NORM(3, 512, 2)
-                          : LLMINT8_NORM(4, 512, 2);
+                          : LLMINT8_NORM(4, 512, 2);   // two go to 256 threads, with four
     return per == 1   ? LLMINT8_NORM(1, 1024, 1)
            : per == 2 ? LLMINT8_NORM(2, 1024, 1)
            : per == 3 ? LLMINT8_NORM(3, 1024, 1)

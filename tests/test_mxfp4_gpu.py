@@ -232,7 +232,8 @@ NORMS = [("rms", None, 0, True, True), ("layer", None, 0, True, True), ("rms", "
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("norm,post,gate,residual,affine", NORMS)
 @pytest.mark.parametrize("M,K", [(1, 32), (2, 4096), (6, 288), (130, 2080), (300, 1056),
-                                 (200, 12288), (2, 32768), (160, 17408)])
+                                 (200, 12288), (2, 32768), (160, 17408), (150, 16384),
+                                 (151, 14368), (149, 768)])
 def test_residual_norm(M, K, norm, post, gate, residual, affine, dtype):
     gate = M if gate == "M" or (gate and M % gate) else gate
     x, a = norm_inputs(M, K, dtype, norm, post, gate, residual, affine, seed=M + K)
