@@ -359,6 +359,37 @@ def test_streams_graphs_and_plans():
         assert torch.equal(out_norm, L.llmint8_mxfp4_linear(Y, wc, ws))
 
 
+def test_a_stream_argument_inside_a_capture():
+    x, w, b, (wc, ws) = layer(20, 520, 512, F16)
+    want = L.llmint8_mxfp4_linear(x, wc, ws, bias=b)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        y = L.llmint8_mxfp4_linear(x, wc, ws, bias=b, stream=side)
+        q = L.llmint8_mxfp4_quantize(x, stream=side)
+        v = L.llmint8_mxfp4_dequant(*q, stream=side)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    assert torch.equal(v, L.llmint8_mxfp4_dequant(*L.llmint8_mxfp4_quantize(x)))
+
+
+def test_inputs_dropped_while_another_stream_works():
+    """Temporaries handed to a call on another stream keep their memory until that stream is done."""
+    x, w, b, (wc, ws) = layer(2000, 2048, 2048, F16, seed=3)
+    want = L.llmint8_mxfp4_linear(x, wc, ws)
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(10):
+        temp = x.clone()
+        side.wait_stream(torch.cuda.current_stream())
+        got.append(L.llmint8_mxfp4_linear(temp, wc, ws, stream=side))
+        del temp
+        torch.full_like(x, 7.0)                 # would take the memory of the one dropped
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in got)
+
+
 def test_two_streams_at_once():
     """Calls that overlap, each with a workspace of its own."""
     layers = [layer(m, 2048, 2048, F16, seed=m) for m in (8, 200, 1500)]
