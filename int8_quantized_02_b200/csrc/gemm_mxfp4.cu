@@ -86,7 +86,8 @@ __device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t saddr) {
 
 // The MMAs of one k-tile.  `n_mma` (1 to 4) leaves out 64-column steps past K.
 // TMEM at `sf`: for each pair of steps 4 columns of A's scales, then 4 for each 128 rows of B, of
-// which B's rows begin at column `b0` (a column holds 32 rows).
+// which B's rows begin at column `b0` (a column holds 32 rows; the address must be even, so tiles
+// of B begin at multiples of 64 rows).
 template <bool PAIR, int M, int N>
 __device__ __forceinline__ void mma_ktile(uint32_t d, uint32_t sa, uint32_t sb, uint32_t ssfa,
                                           uint32_t ssfb, uint32_t sf, uint32_t b0, int n_mma,
@@ -525,7 +526,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
     const int S = a.splits;
     const int rank = (int)(blockIdx.x % (unsigned)S);
     const int band = (int)(blockIdx.x / (unsigned)S);
-    const int m0 = (int)blockIdx.y * NT;
+    const int m0 = (int)blockIdx.y * NT;               // more than one tile only with NT = 64
     // this CTA's k-tiles
     const int k_begin = (int)((int64_t)a.tiles_k * rank / S);
     const int k_count = (int)((int64_t)a.tiles_k * (rank + 1) / S) - k_begin;
