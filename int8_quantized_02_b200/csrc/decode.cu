@@ -61,13 +61,17 @@ constexpr int QKB = 8;
 // chain fast (1 stage starves the stream, 3 or 5 slow the chain; 2 measured best).
 constexpr int DINFLIGHT = 2;
 constexpr int SMEM_LIMIT = 232448;      // 227 KB opt-in per CTA
-// Two MMA issuers per CTA (warps 1 and 3): issuer i takes the weight stages j with
-// j % 2 == i of every tile, into its own int32 accumulator of 16 columns; the epilogue adds the
-// two (exact).  Measured on B200: one thread issues a 128 x 16 x 32 MMA about every 60 cycles,
-// two threads together one every 40 (the tensor pipe's floor for this shape), and a
-// tcgen05.commit costs about 150 cycles; with one issuer the k-loop, not HBM, bounded a call.
-// Each issuer issues 8 MMAs per wait and per commit.  Accumulators are double-buffered over
-// tiles: column (acc * 2 + issuer) * 16.
+// Two MMA issuers per CTA (warps 1 and 3): issuer i takes the weight stages g with g % 2 ==
+// i, counted over all tiles of the CTA, into its own int32 accumulator of 16 columns; the
+// epilogue adds the two (exact).  The rings have an even number of stages, so every use of
+// a stage is the same issuer's, which has seen the use before it: a parity wait cannot tell
+// a phase from the one two before, and copies may land out of order, so an issuer that took
+// over a stage whose last copy is still on its way would not wait for its own.  Measured on
+// B200: one thread issues a 128 x 16 x 32 MMA about every 60 cycles, two threads together
+// one every 40 (the tensor pipe's floor for this shape), and a tcgen05.commit costs about
+// 150 cycles; with one issuer the k-loop, not HBM, bounded a call. Each issuer issues 8
+// MMAs per wait and per commit.  Accumulators are double-buffered over tiles: column (acc *
+// 2 + issuer) * 16.
 constexpr uint32_t DTMEM_COLS = 64;
 
 __device__ __forceinline__ void unpack8(const uint4 &v, float *f) {
@@ -586,10 +590,10 @@ llmint8_decode_kernel(const __grid_constant__ CUtensorMap tmCB, const DArgs a) {
                     const int kb0 = sj * DKS, nkb = min(DKS, a.kblocks - kb0);
                     // at most `inflight` stages on their way while X is quantized: a short
                     // memory queue keeps the latency of everything else on the GPU (X, the
-                    // tables, the image) low; once the MMAs run, up to four (fewer than the
-                    // ring's stages, so the stage waited on is still that use's)
+                    // tables, the image) low; once the MMAs run, up to four (no more than
+                    // the ring's stages, so the stage waited on is still that use's)
                     const int depth = *reinterpret_cast<volatile int *>(&tail->streaming)
-                                          ? min(4, S - 1) : a.inflight;
+                                          ? min(4, S) : a.inflight;
                     if (issued >= depth) {
                         const int prev = issued - depth;
                         if (!wait(smem_addr(&tail->full[prev % S]), (uint32_t)(prev / S) & 1u))
@@ -632,8 +636,9 @@ llmint8_decode_kernel(const __grid_constant__ CUtensorMap tmCB, const DArgs a) {
                 const uint32_t d = tmem + (uint32_t)((acc * 2 + issuer) * DM);
                 const int rot = rot_of(tile);
                 bool first = true;
-                for (int j = issuer; j < a.nst; j += 2) {
-                    const int g = tl_ * a.nst + j;               // stage in the producer's order
+                const int g0 = tl_ * a.nst;                      // stages in the producer's order
+                for (int j = a.nst >= 2 ? (issuer ^ g0) & 1 : 0; j < a.nst; j += 2) {
+                    const int g = g0 + j;
                     const int stage = g % S;
                     const uint32_t phase = (uint32_t)(g / S) & 1u;
                     int sj = j + rot;
@@ -886,7 +891,8 @@ DecodePlan decode_plan(int64_t M, int64_t N, int64_t K, int64_t cap, int sms) {
     p.nst = (int)ceil_div(p.kblocks, DKS);
     const int64_t istage = (int64_t)DKS * p.rows * DBK;
     p.resident = p.nst <= DIMG_MAX && p.nst * istage <= DIMG_BYTES;
-    p.nistage = p.resident ? p.nst : (int)std::min<int64_t>(DIMG_MAX, DIMG_BYTES / istage);
+    p.nistage = p.resident ? p.nst                      // a ring of 16 or 32, even too
+                           : (int)std::min<int64_t>(DIMG_MAX, DIMG_BYTES / istage);
     const int64_t img = align_up((int64_t)p.nistage * istage + (p.rows == 8 ? 1024 : 0), 1024);
     p.tail_off = (uint32_t)img;
     p.xo_off = (uint32_t)align_up(p.tail_off + (int64_t)sizeof(DTail), 16);
@@ -895,6 +901,7 @@ DecodePlan decode_plan(int64_t M, int64_t N, int64_t K, int64_t cap, int sms) {
     const int64_t slack = (int64_t)(DMMA_M - p.Rt) * DBK;
     const int64_t room = SMEM_LIMIT - 1024 - (int64_t)p.ring_off - slack;
     p.stages = (int)std::max<int64_t>(0, std::min<int64_t>(DMAX_STAGES, room / stage));
+    p.stages &= ~1;                        // even: each stage keeps its MMA issuer
     p.inflight = std::max(1, std::min(DINFLIGHT, p.stages));
     // a quantizer: tables, its slice of X, the image of its k-blocks
     const int64_t qsmem = QX_OFF + M * p.bpq * DBK * 2 + (int64_t)p.bpq * p.rows * DBK + 1024;
