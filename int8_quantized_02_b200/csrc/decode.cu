@@ -560,10 +560,15 @@ llmint8_decode_kernel(const __grid_constant__ CUtensorMap tmCB, const DArgs a) {
         fence_mbar_init();
         tma_prefetch_desc(&tmCB);
     }
-    if (warp == 1) tmem_alloc(smem_addr(&tail->tmem_base), DTMEM_COLS);
-    // the next call's kernel may launch now (it waits for this grid before it reads or
-    // writes anything); this one waits for the previous grid before it touches memory
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 1) {
+        tmem_alloc(smem_addr(&tail->tmem_base), DTMEM_COLS);
+        // the next call's kernel may launch now (it waits for this grid before it reads or
+        // writes anything), and not before this CTA has its columns of TMEM, so this warp alone
+        // says so: a dependent that took them first would wait for this grid, and this grid's
+        // allocation for the dependent
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
+    // this kernel waits for the previous grid before it touches memory
     asm volatile("griddepcontrol.wait;" ::: "memory");
     tc_fence_before();
     __syncthreads();

@@ -461,7 +461,8 @@ struct Band {
     // Stages of a CTA that has an SM, or half of one, to itself: about 100 KB, so that two fit; and
     // where the grid fills the machine more than twice, about 60 KB, so that a third CTA covers the
     // others' first loads and last stores (8 x 49152 x 12288: 53.7 us with 5 stages, 50.2 with 3).
-    // TMEM never runs out: the CTAs that fit an SM's shared memory hold 512 columns at most.
+    // The CTAs of one such grid that fit an SM's shared memory hold 512 columns of TMEM at most, so none of
+    // them waits for another's.
     static constexpr int STAGES = 104 * 1024 / STAGE;
     static constexpr int FEW = NT == 64 ? 2 : 3;
     static constexpr uint32_t SF = NT;                 // TMEM: accumulator, then the scales
@@ -538,8 +539,6 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         return k_begin + (k >= k_count ? k - k_count : k);
     };
 
-    // the next kernel may set up, and ask L2 for its weight, while this one runs
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         for (int s = 0; s < stages; ++s) {
             mbar_init(smem_addr(&tail->full[s]), 1);
@@ -556,7 +555,14 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             tma_prefetch_desc(&tmXS);
         }
     }
-    if (warp == 1) tmem_alloc(smem_addr(&tail->tmem_base), C::COLS);
+    if (warp == 1) {
+        tmem_alloc(smem_addr(&tail->tmem_base), C::COLS);
+        // The next kernel may set up, and ask L2 for its weight, while this one runs.  Not before this
+        // CTA has its columns of TMEM, so the warp that allocates them says so (one thread's word
+        // counts for the CTA): a dependent that took them first would wait for this grid, and this
+        // grid's allocation for the dependent.
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
