@@ -341,10 +341,6 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmA, const CUtensor
             if (PAIR) tc_commit_pair_both(smem_addr(&tail->mma_done));
             else tc_commit(smem_addr(&tail->mma_done));
             drain_wait(smem_addr(&tail->mma_done), 0, a.status);
-        } else if (lane == 0) {
-            // second CTA of a pair: its TMEM and shared memory are the leader's MMA operands
-            // until the leader's last MMA has completed
-            drain_wait(smem_addr(&tail->mma_done), 0, a.status);
         }
     } else {
         // ----------------------------------------------------------------- epilogue ----
@@ -545,6 +541,11 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmA, const CUtensor
         }
     }
     if (warp == 1) {
+        // second CTA of a pair: its TMEM and shared memory are the leader's MMA operands until
+        // the leader's last MMA has completed (this wait has a fixed limit, so it begins only
+        // now: the launch itself may take longer than that)
+        if (PAIR && !leader && lane == 0) drain_wait(smem_addr(&tail->mma_done), 0, a.status);
+        __syncwarp();
         tc_fence_after();
         if (PAIR) tmem_dealloc_pair(tmem, TMEM_COLS);
         else tmem_dealloc(tmem, TMEM_COLS);

@@ -130,7 +130,7 @@ struct PairTail {
     uint64_t shared_empty;               // the columns both accumulators hold are read out
     uint64_t mma_done;
     uint64_t peer_loads;                 // leader: peer_issued holds the second CTA's count
-    uint64_t loads_drained;              // second CTA: the leader drained every load
+    uint64_t loads_drained;              // second CTA: the leader is done, its loads drained
     uint64_t peer_exit;                  // leader: the second CTA made its last arrive
     uint32_t tmem_base;
     uint32_t peer_issued;
@@ -263,7 +263,6 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 for (uint32_t it = all - min(all, (uint32_t)P_STAGES); it < all; ++it)
                     drain_wait(smem_addr(&tail->full[it % P_STAGES]), (it / P_STAGES) & 1u,
                                a.status);
-                mbar_arrive_cluster(map_to_rank(smem_addr(&tail->loads_drained), 1));
             } else {
                 st_cluster_u32(map_to_rank(smem_addr(&tail->peer_issued), 0), issued);
                 mbar_arrive_cluster(map_to_rank(smem_addr(&tail->peer_loads), 0));
@@ -271,10 +270,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         }
     } else if (warp == 1) {
         // --------------------------------------------------------------- MMA issuer ----
-        if (!leader) {
-            // the second CTA's TMEM and shared memory are the leader's MMA operands until then
-            if (lane == 0) drain_wait(smem_addr(&tail->mma_done), 0, a.status);
-        } else if (elect_one()) {
+        if (leader && elect_one()) {
             int stage = 0;
             uint32_t phase = 0, acc_phase = 0;
             int acc = 0, done = 0;
@@ -435,8 +431,15 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
 
     tc_fence_before();
     __syncthreads();
+    // Winding down.  The waits from here on have a fixed limit, so they begin only now: a launch may take
+    // longer than that, and the two CTAs reach this point at nearly the same time.
     if (threadIdx.x == 0) {
+        // a CTA that gave up takes the other along (which is still there: the leader until peer_exit,
+        // the second CTA until loads_drained)
+        if (tail->abort_flag)
+            st_cluster_u32(map_to_rank(smem_addr(&tail->abort_flag), rank ^ 1u), 1u);
         if (leader) {
+            mbar_arrive_cluster(map_to_rank(smem_addr(&tail->loads_drained), 1));
             // the second CTA has made its last arrive on this CTA's barriers
             drain_wait(smem_addr(&tail->peer_exit), 0, a.status);
         } else {
@@ -446,6 +449,10 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         }
     }
     if (warp == 1) {
+        // the second CTA's TMEM and shared memory are the leader's MMA operands until its last MMA has
+        // completed
+        if (!leader && lane == 0) drain_wait(smem_addr(&tail->mma_done), 0, a.status);
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
