@@ -441,7 +441,8 @@ LLMINT8_API llmint8_status llmint8_mxfp4_linear_quantized(const uint8_t *Xc, con
  *              length has one each.  gate_rows must divide M.
  *   norm       LLMINT8_NORM_NONE leaves y out (Y, codes and scales must then be NULL).  weight,
  *              bias: [K] or NULL.
- *   eps        >= 0, for both norms.
+ *   eps        >= 0, for both norms.  Rows may be of any size: those whose squares leave fp32's range
+ *              (bf16's can) are scaled by a power of two for their sums.
  *   H, Y       [M, K] outputs, or NULL.  Each may be X's or the residual's own (dense) buffer, but not
  *              both the same; any other overlap of an output is refused.
  *   codes, scales  MXFP4 form of y (both or neither NULL), padding included.
