@@ -78,6 +78,7 @@ mxfp4_dequant_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restri
     const Place p(wpr_log2);
     const uint32_t ch = p.kt * 32 + lane;
     if (ch >= chunks || p.row >= R) return;
+    const uint32_t here = min(chunks - p.kt * 32, 32u);       // lanes that go on, from 0
     uint32_t q[kRows];
     const uint32_t *at = codes + (uint64_t)p.row * chunks + ch;
 #pragma unroll
@@ -119,7 +120,7 @@ mxfp4_dequant_kernel(const uint32_t *__restrict__ codes, const uint8_t *__restri
             float g[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                g[e] = __shfl_xor_sync(__activemask(), odd ? f[e] : f[4 + e], 1);
+                g[e] = __shfl_xor_sync(0xffffffffu >> (32 - here), odd ? f[e] : f[4 + e], 1);
             float4 *pair = reinterpret_cast<float4 *>(o + (uint64_t)(32 * j) * pitch) - (odd ? 1 : 0);
             pair[0] = odd ? make_float4(g[0], g[1], g[2], g[3]) : make_float4(f[0], f[1], f[2], f[3]);
             pair[2] = odd ? make_float4(f[4], f[5], f[6], f[7]) : make_float4(g[0], g[1], g[2], g[3]);

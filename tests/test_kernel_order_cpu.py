@@ -2,7 +2,8 @@
 
 A kernel that lets its programmatic dependents launch before it holds its tensor memory can hang: a
 dependent placed on the same SM may allocate the columns first and then wait for this grid, whose
-allocation waits for the dependent's columns."""
+allocation waits for the dependent's columns.  A shuffle that takes the lanes that happen to be active
+for its own is undefined once they have diverged."""
 from __future__ import annotations
 
 import glob
@@ -48,3 +49,8 @@ def test_dependents_launch_after_the_allocation(name, body):
         between = body[alloc:m.start()]       # the same block, or behind a barrier
         assert "}" not in between or "__syncthreads()" in between, \
             "another warp may let them launch before the allocating one is done"
+
+
+def test_shuffles_name_their_lanes():
+    for p in glob.glob(os.path.join(build_mod.CSRC, "*.cu*")):
+        assert "__activemask" not in open(p).read(), os.path.basename(p)
