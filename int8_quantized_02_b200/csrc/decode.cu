@@ -95,6 +95,13 @@ __device__ __forceinline__ uint32_t xq_offset(int m, int c0) {
 
 __host__ __device__ constexpr int image_rows(int M) { return M <= 8 ? 8 : kDecodeMaxM; }
 
+// Stages of an image ring (used when the image does not fit): an even number, as of the weight ring, so
+// that each keeps its MMA issuer.
+constexpr int image_ring(int rows) {
+    return DIMG_BYTES / (DKS * rows * DBK) < DIMG_MAX ? DIMG_BYTES / (DKS * rows * DBK) : DIMG_MAX;
+}
+static_assert(image_ring(8) % 2 == 0 && image_ring(kDecodeMaxM) % 2 == 0, "even image rings");
+
 // Descriptor of an image block at `saddr` (+ k offset) for the 16-column MMA operand: the two
 // 8-row groups are `sbo` bytes apart (1024 in a 16-row block; for an 8-row block the distance
 // to the zero atom, so that rows 8..15 read as zeros).
@@ -896,8 +903,7 @@ DecodePlan decode_plan(int64_t M, int64_t N, int64_t K, int64_t cap, int sms) {
     p.nst = (int)ceil_div(p.kblocks, DKS);
     const int64_t istage = (int64_t)DKS * p.rows * DBK;
     p.resident = p.nst <= DIMG_MAX && p.nst * istage <= DIMG_BYTES;
-    p.nistage = p.resident ? p.nst                      // a ring of 16 or 32, even too
-                           : (int)std::min<int64_t>(DIMG_MAX, DIMG_BYTES / istage);
+    p.nistage = p.resident ? p.nst : image_ring(p.rows);
     const int64_t img = align_up((int64_t)p.nistage * istage + (p.rows == 8 ? 1024 : 0), 1024);
     p.tail_off = (uint32_t)img;
     p.xo_off = (uint32_t)align_up(p.tail_off + (int64_t)sizeof(DTail), 16);
