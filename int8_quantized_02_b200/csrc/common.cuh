@@ -180,7 +180,7 @@ struct BoundedWait {
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
         if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t0 = global_timer_ns();
-        for (uint32_t it = 1;; ++it) {
+        for (uint32_t it = 0;; ++it) {
             if (mbar_try_wait(bar, parity)) return true;
             if ((it & 63u) == 0u) {
                 if (*abort_flag) return false;
