@@ -82,9 +82,11 @@ struct Tail {
     uint64_t mma_done;
     uint64_t slice_full;                // the epilogue warps staged the column slice
     uint64_t slice_empty;               // ... and are done reading it
-    uint64_t loads_drained;             // pair, second CTA: the leader drained every load
+    uint64_t peer_loads;                // pair, leader: peer_issued holds the second CTA's count
+    uint64_t loads_drained;             // pair, second CTA: the leader is done, its loads drained
     uint64_t peer_exit;                 // pair, leader: the second CTA made its last arrive
     uint32_t tmem_base;
+    uint32_t peer_issued;
     int abort_flag;
 };
 template <bool PAIR>
@@ -179,6 +181,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmA, const CUtensor
         mbar_init(smem_addr(&tail->mma_done), 1);
         mbar_init(smem_addr(&tail->slice_full), EPI_WARPS);
         mbar_init(smem_addr(&tail->slice_empty), EPI_WARPS);
+        mbar_init(smem_addr(&tail->peer_loads), 1);
         mbar_init(smem_addr(&tail->loads_drained), 1);
         mbar_init(smem_addr(&tail->peer_exit), 1);
         tail->abort_flag = 0;
@@ -225,8 +228,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmA, const CUtensor
         if (lane == 0) {
             const uint64_t keep = l2_policy_evict_last();
             int stage = 0;
-            uint32_t phase = 0;
-            uint32_t used = 0, last_parity = 0;   // per stage: issued at least once / parity
+            uint32_t phase = 0, issued = 0;       // stages whose loads are on their way
             for (int tile = unit; tile < total_tiles; tile += units) {
                 // this CTA's rows of X and of the weight tile
                 const int m0 = (tile % a.tiles_m) * C::TILE_M + (int)rank * BM;
@@ -257,8 +259,7 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmA, const CUtensor
                             tma_load_2d(sa + A_BYTES, &tmWo, x, n0, full);
                         }
                     }
-                    used |= 1u << stage;
-                    last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+                    ++issued;
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1;
@@ -266,13 +267,31 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmA, const CUtensor
                 }
             }
         drain:
-            // wait for every copy this thread issued to land before the CTA may exit (a pair's
-            // leader waits for the copies of both CTAs, then tells the second CTA)
+            // Every copy lands before its CTA may exit; a pair's leader sees to those of both, which
+            // signal its barriers.  After a wait that gave up, one CTA of a pair may have issued
+            // stages that the other did not: the leader then takes the missing copies' bytes off,
+            // or expects those it did not.
+            uint32_t all = issued;
+            if (PAIR) {
+                if (tail->abort_flag)
+                    st_cluster_u32(map_to_rank(smem_addr(&tail->abort_flag), rank ^ 1u), 1u);
+                if (leader) {
+                    drain_wait(smem_addr(&tail->peer_loads), 0, a.status);
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    const uint32_t theirs = *reinterpret_cast<volatile uint32_t *>(&tail->peer_issued);
+                    for (uint32_t it = theirs; it < issued; ++it)
+                        mbar_complete_tx(smem_addr(&tail->full[it % STAGES]), STAGE_BYTES);
+                    for (uint32_t it = issued; it < theirs; ++it)
+                        mbar_arrive_expect_tx(smem_addr(&tail->full[it % STAGES]), STAGE_BYTES);
+                    all = max(issued, theirs);
+                } else {
+                    st_cluster_u32(map_to_rank(smem_addr(&tail->peer_issued), 0), issued);
+                    mbar_arrive_cluster(map_to_rank(smem_addr(&tail->peer_loads), 0));
+                }
+            }
             if (!PAIR || leader) {
-                for (int s = 0; s < STAGES; ++s)
-                    if (used & (1u << s))
-                        drain_wait(smem_addr(&tail->full[s]), (last_parity >> s) & 1u, a.status);
-                if (PAIR) mbar_arrive_cluster(map_to_rank(smem_addr(&tail->loads_drained), 1));
+                for (uint32_t it = all - min(all, (uint32_t)STAGES); it < all; ++it)
+                    drain_wait(smem_addr(&tail->full[it % STAGES]), (it / STAGES) & 1u, a.status);
             }
         }
     } else if (warp == 1) {
@@ -531,7 +550,12 @@ __device__ __forceinline__ void gemm_body(const CUtensorMap &tmA, const CUtensor
     tc_fence_before();
     __syncthreads();
     if (PAIR && threadIdx.x == 0) {
+        // a CTA that gave up takes the other along (which is still there: the leader until
+        // peer_exit, the second CTA until loads_drained)
+        if (tail->abort_flag)
+            st_cluster_u32(map_to_rank(smem_addr(&tail->abort_flag), rank ^ 1u), 1u);
         if (leader) {
+            mbar_arrive_cluster(map_to_rank(smem_addr(&tail->loads_drained), 1));
             // the second CTA has made its last arrive on this CTA's barriers
             drain_wait(smem_addr(&tail->peer_exit), 0, a.status);
         } else {

@@ -46,3 +46,19 @@ def test_mxfp4(M, N, K, tiny_limit):
     out = torch.full((M + 2, N), 7.0, dtype=torch.float16, device="cuda")
     seen = run_out(tiny_limit, lambda: L.llmint8_mxfp4_linear(X, WC, WS, Y=out[1:M + 1], workspace=ws), ws, out)
     assert set(seen) <= {L.OK, L.ERR_TIMEOUT} and L.ERR_TIMEOUT in seen
+
+
+# single CTAs, CTA pairs (outlier columns in the epilogue, and on the tensor cores), the decode kernel
+@pytest.mark.parametrize("M,N,K,outliers", [(100, 512, 16384, 3), (200, 512, 16384, 3), (1500, 1024, 16384, 0),
+                                            (3000, 4096, 4096, 3), (3000, 4096, 4096, 40), (16, 4096, 4096, 3)])
+def test_int8(M, N, K, outliers, tiny_limit):
+    g = torch.Generator(device="cuda").manual_seed(M)
+    X = torch.randn((M, K), generator=g, device="cuda").half().clamp(-5, 5)
+    X[:, 7:7 + 5 * outliers:5] = 10
+    CB = torch.randint(-127, 128, (N, K), generator=g, dtype=torch.int8, device="cuda")
+    SCB = torch.rand(N, generator=g, device="cuda") * 0.1
+    ws = torch.empty(L.llmint8_linear_workspace_size(M, N, K, 64), dtype=torch.uint8, device="cuda")
+    out = torch.full((M + 2, N), 7.0, dtype=torch.float16, device="cuda")
+    seen = run_out(tiny_limit, lambda: L.llmint8_linear(X, CB, SCB, max_outliers=64, Y=out[1:M + 1], workspace=ws),
+                   ws, out)
+    assert set(seen) <= {L.OK, L.ERR_TIMEOUT} and L.ERR_TIMEOUT in seen
