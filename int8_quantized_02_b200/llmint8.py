@@ -770,6 +770,8 @@ def _residual_norm(X, residual, weight, bias, norm, post_norm, post_weight, post
     dev, dt = X.device, X.dtype
     if norm not in NORMS or post_norm not in NORMS:
         raise ValueError(f"norm and post_norm are one of {', '.join(map(repr, NORMS))}")
+    if norm is None and Y is not None:
+        raise ValueError("without a norm there is no Y to write")
     pr, ldr = None, K
     if residual is not None:
         if residual.shape != X.shape or residual.device != dev:
