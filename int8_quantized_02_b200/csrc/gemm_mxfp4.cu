@@ -222,6 +222,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 const int nt = (tile / a.tiles_m) * 2;               // the tile's 256 of W
                 int kr = first_kblock(tile / a.tiles_m, a.tiles_k);
                 for (int kb = 0; kb < a.tiles_k; ++kb) {
+                    LLMINT8_DCHECK(kr >= 0 && kr < a.tiles_k && nt / 2 < a.tiles_n, a.status);
                     if (!wait(smem_addr(&tail->empty[stage]), phase ^ 1)) goto drain;
                     const uint32_t full = smem_addr(&tail->full[stage]);
                     const uint32_t sa = smem_addr(smem + stage * P_STAGE);
@@ -388,6 +389,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                     fence_proxy_async_shared();
                     __syncwarp();
                     // what lies past M or N is left out by the tensor map
+                    LLMINT8_DCHECK(m0 >= 0 && nb >= 0 && nb < a.N, a.status);
                     if (lane == 0 && m0 < a.M) tma_store_2d(&tmY, smem_addr(stg), nb, m0);
                     continue;
                 }
@@ -395,6 +397,7 @@ mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
                 // where rows start on 4 bytes
                 __syncwarp();
                 const int rows = min(32, a.M - m0);
+                LLMINT8_DCHECK(rows <= 32 && (rows <= 0 || m0 + rows <= a.M), a.status);
                 uint16_t *y = static_cast<uint16_t *>(a.Y) + (int64_t)m0 * a.N;
                 const auto word_at = [&](int r, int w) {
                     return stg + r * 64 + (((w >> 2) ^ ((r >> 1) & 3)) << 4) + (w & 3) * 4;
@@ -581,6 +584,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
         const uint32_t full = smem_addr(&tail->full[stage]);
         const uint32_t sa = smem_addr(smem + stage * C::STAGE);
         const int kt = ktile(it);
+        LLMINT8_DCHECK(kt >= k_begin && kt < k_begin + k_count && stage < stages, a.status);
         mbar_arrive_expect_tx(full, FUSED ? ROWS * KB + kMxTile : C::STAGE);
         tma_load_2d(sa, &tmW, kt * KB, band * ROWS, full);
         tma_load_2d(sa + (ROWS + NT) * KB, &tmWS, 0, band * a.tiles_k + kt, full);
@@ -651,6 +655,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             for (int it = warp - 2; it < k_count; it += turns) {
                 const int stage = it % stages;
                 const int64_t ch = (int64_t)ktile(it) * 32 + lane;
+                LLMINT8_DCHECK(stage < stages && a.M <= kMxfp4FusedRows && ktile(it) < a.tiles_k, a.status);
                 Chunk<DT> c[kMxfp4FusedRows];
 #pragma unroll
                 for (int m = 0; m < kMxfp4FusedRows; ++m)
@@ -729,6 +734,7 @@ mxfp4_band_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant
             }
         }
         const int64_t o = (int64_t)(m0 + m) * a.N + n;
+        LLMINT8_DCHECK(m < NT && m0 + m < a.M && ((a.N & 3) || n >= a.N || n + 4 <= a.N), a.status);
         if ((a.N & 3) == 0) {
             if (n < a.N)
                 *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.Y) + o) =
