@@ -25,6 +25,8 @@
  *     Conditions found on the device (outlier capacity exceeded, a bounded wait that timed
  *     out) are written to the status word of the workspace; read them with
  *     llmint8_device_status().  Each call that takes a workspace overwrites that word.
+ *     (Calls may be captured into a CUDA graph and replayed.  A replay is no new call in one
+ *     respect: after a replay whose wait timed out, later ones report that too.)
  *   - Shapes: M >= 1; K and N are multiples of 16 and >= 16; K <= 131072 (so that
  *     |C| <= K * 127^2 < 2^31).  Violations return LLMINT8_ERR_UNSUPPORTED_SHAPE.  (The MXFP4
  *     calls and the residual norm at the end of this file state their own shapes.)

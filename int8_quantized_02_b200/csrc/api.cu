@@ -581,8 +581,9 @@ llmint8_status llmint8_workspace_outlier_weights(const void *ws, int64_t M, int6
 // library routine.
 //
 // Nothing in it needs clearing between calls: every call tags its status words and its table
-// with a fresh call epoch (the counter only grows and starts above zero), and the outlier
-// count is plain-stored by each call.  Calls in stream order are safe: the decode kernel of a
+// with a fresh call epoch (the counter only grows and starts above zero), the outlier count is
+// plain-stored by each call, and the kernel clears the table's tags itself (a graph replays one
+// epoch).  Calls in stream order are safe: the decode kernel of a
 // call writes the scratch only after the previous grid on its stream has finished.  Calls
 // that overlap - on two streams, or from two host threads without stream order between them -
 // share the one scratch of their device and race on its table; their outputs are undefined.

@@ -254,6 +254,9 @@ __device__ __forceinline__ unsigned long long relaxed_load(const unsigned long l
     asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(w) : "memory");
     return v;
 }
+__device__ __forceinline__ void count_reader(unsigned long long *w) {
+    asm volatile("red.relaxed.gpu.global.add.u64 [%0], %1;" ::"l"(w), "l"(1ull) : "memory");
+}
 // Bounded, backed-off poll by one thread until each of the n <= kDecodeMaxQuantizers words
 // holds v.  Each round loads the words together (relaxed); the fence after the round that
 // finds them all makes this thread acquire what their writers released.  False, with the
@@ -512,9 +515,25 @@ __device__ void quantize_x(const DArgs &a, uint8_t *smem) {
     }
     __syncthreads();
     if (threadIdx.x == 0) {
+        if (qi == 0) relaxed_store(&a.table->readers, 0ull);
         bulk_store_wait();
         fence_proxy_async_global();
         release_word(&a.table->done[qi], a.epoch);
+        if (qi == 0) {
+            // Once every poller is through (and so every quantizer has read the partials), clear the
+            // words that carry the call's number.  Nothing waits for this thread; if a poller gave
+            // up, it does too.
+            const unsigned long long all = 2ull * (gridDim.x - a.nq);
+            const uint64_t t0 = global_timer_ns();
+            while (relaxed_load(&a.table->readers) != all) {
+                if (global_timer_ns() - t0 > a.timeout_ns) return;
+                __nanosleep(64);
+            }
+            for (int j = 0; j < a.nq; ++j) {
+                relaxed_store(&a.table->done[j], 0ull);
+                for (int mm = 0; mm <= DM; ++mm) relaxed_store(&a.table->part[j][mm], 0ull);
+            }
+        }
     }
 }
 
@@ -705,6 +724,7 @@ llmint8_decode_kernel(const __grid_constant__ CUtensorMap tmCB, const DArgs a) {
         __syncwarp();
         if (lane == 0 &&
             poll_all(a.table->done, a.nq, a.epoch, a.status, a.timeout_ns, &tail->abort_flag)) {
+            count_reader(&a.table->readers);
             fence_proxy_async_global();           // the image is read by the async proxy
             const int ntiles = (a.tiles - band0 + bands - 1) / bands;   // tiles of this CTA
             const int nstg = a.resident ? a.nst : ntiles * a.nst;
@@ -743,8 +763,10 @@ llmint8_decode_kernel(const __grid_constant__ CUtensorMap tmCB, const DArgs a) {
         // on tbar; lane 0 of each epilogue warp acquires that by its wait on tbar, and the
         // __syncwarp orders it before the reads of its other lanes
         if (et == 0 &&
-            poll_all(a.table->done, a.nq, a.epoch, a.status, a.timeout_ns, &tail->abort_flag))
+            poll_all(a.table->done, a.nq, a.epoch, a.status, a.timeout_ns, &tail->abort_flag)) {
+            count_reader(&a.table->readers);
             mbar_arrive(smem_addr(&tail->tbar));
+        }
         int ok = 0;
         if (lane == 0) ok = wait(smem_addr(&tail->tbar), 0) ? 1 : 0;
         ok = __shfl_sync(0xffffffffu, ok, 0);

@@ -87,7 +87,10 @@ constexpr int kDecodeMaxOutliers = 256;
 //               the call's number carries its value;
 //   done[q]     the call's number, stored with release semantics once quantizer q's k-blocks of
 //               the operand image and its entries of idx are written (quantizer 0: also sca,
-//               total and n_out).
+//               total and n_out);
+//   readers     the streamers' threads that have seen every done word; after the last of them
+//               quantizer 0 clears part and done, so that a call replayed from a graph, under the
+//               number it was captured with, does not take the last replay's words for its own.
 constexpr int kDecodeMaxQuantizers = 8;
 struct DecodeTable {
     unsigned long long done[kDecodeMaxQuantizers];
@@ -96,6 +99,7 @@ struct DecodeTable {
     int32_t n_out;                            // ... of them listed (<= capacity)
     float sca[kDecodeMaxM];                   // row absmax over the regular columns
     int32_t idx[kDecodeMaxOutliers];          // outlier columns, ascending
+    unsigned long long readers;
 };
 
 // Bytes of the int8 operand image the quantizer writes: one block of 16 rows (8 when M <= 8)
