@@ -531,7 +531,7 @@ __device__ void quantize_x(const DArgs &a, uint8_t *smem) {
             }
             for (int j = 0; j < a.nq; ++j) {
                 relaxed_store(&a.table->done[j], 0ull);
-                for (int mm = 0; mm <= DM; ++mm) relaxed_store(&a.table->part[j][mm], 0ull);
+                for (int mm = 0; mm <= DM; ++mm) relaxed_store(&a.table->part[j][mm], ~tag);
             }
         }
     }
