@@ -290,9 +290,9 @@ LLMINT8_API llmint8_status llmint8_set_wait_timeout_ns(uint64_t ns);
  * kernel of a call with CUDA events and count launches):
  *   llmint8_set_profile_events(start, stop): two cudaEvent_t.  While both are non-NULL,
  *     every llmint8_linear, llmint8_linear_next_bitmaps, llmint8_linear_with_bitmaps,
- *     llmint8_linear_noalloc, llmint8_mxfp4_linear and llmint8_mxfp4_linear_quantized call records `start` on its stream immediately before its
- *     product kernel (the GEMM; on the decode path, the decode kernel) and `stop`
- *     immediately after it.  NULL, NULL disables.
+ *     llmint8_linear_noalloc, llmint8_mxfp4_linear and llmint8_mxfp4_linear_quantized call
+ *     records `start` on its stream immediately before its product kernel (the GEMM; on the
+ *     decode path, the decode kernel) and `stop` immediately after it.  NULL, NULL disables.
  *     Process-wide; the caller owns the events and must keep them alive while set.
  *   llmint8_kernel_launch_count(): number of kernels this library has launched in the
  *     process so far.

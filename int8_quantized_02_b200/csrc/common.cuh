@@ -38,8 +38,10 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
 
 // Programmatic dependent launch: every kernel of a layer call is launched so that its CTAs
 // may start while the previous kernel in the stream finishes.  Each waits for that kernel
-// (and so for everything before it) before it touches global memory, and lets the next one
-// launch right away.
+// (and so for everything before it) before it reads or writes global memory (the MXFP4 band
+// kernel asks L2 to fetch weights before that), and lets the next one launch early; one that
+// allocates tensor memory does so first (a dependent could otherwise take the columns and then
+// wait for this grid, which waits for them).
 __device__ __forceinline__ void pdl_wait_then_release() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -171,7 +173,8 @@ inline float fp16_rounded_threshold_f32(float t) {
 
 // Every wait of a pipeline goes through this: it gives up after `timeout_ns`, or as soon
 // as another thread of the CTA gave up, records LLMINT8_ERR_TIMEOUT in the workspace
-// status word and returns false so that the caller can wind the kernel down.
+// status word and returns false so that the caller can wind the kernel down.  A poll may sleep
+// for microseconds, so the clock is read from the second failed one on.
 struct BoundedWait {
     volatile int *abort_flag;   // shared memory, one per CTA
     StatusRef status;
@@ -195,7 +198,7 @@ struct BoundedWait {
 };
 
 // Wait used while winding down (draining copies / MMAs still in flight): ignores the abort
-// flag, bounded by a fixed limit.
+// flag, bounded by a fixed limit, so never begun before the work itself is done or given up.
 __device__ __forceinline__ bool drain_wait(uint32_t bar, uint32_t parity, StatusRef status) {
     constexpr uint64_t kDrainNs = 1000000000ull;
     const uint64_t t0 = global_timer_ns();

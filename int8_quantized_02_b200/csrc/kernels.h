@@ -148,10 +148,6 @@ struct DecodeLaunch {
 };
 cudaError_t launch_decode(const DecodeLaunch &d, cudaStream_t s);
 
-}  // namespace llmint8
-
-namespace llmint8 {
-
 // MXFP4 (mxfp4.cu): codes uint8 [R, K/2], scales uint8 [ceil(R/128)][ceil(K/256)][1024].  dtype is
 // a llmint8_dtype.  pad: the scales of every row up to a multiple of 128 are written (zero past R);
 // without it some stay as they are.

@@ -24,6 +24,7 @@ namespace llmint8 {
 namespace {
 
 constexpr int kMaxWarps = 32;
+constexpr int kSms = 148;                // of a B200; nothing but speed depends on it
 // A mean square (with eps) from here on has lost nothing to squares below fp32's range: those are under
 // 2^-126 each.
 constexpr float kLeastSquare = 0x1p-100f;
@@ -285,7 +286,7 @@ residual_norm_kernel(const __grid_constant__ NormArgs a, int tpr_log2) {
     // through this wave's sums too (4096 x 12288 layer norm: 69.7 us without, 66.3 with).  Not beside
     // the MXFP4 form, whose arithmetic is the bound instead (2048 x 4096: 13.3 and 14.0).
     if (t == 0 && !a.codes) {
-        const uint32_t next = row + 148 * CTAS / 2 * rows;
+        const uint32_t next = row + kSms * CTAS / 2 * rows;
         if (next < a.M) {
             prefetch_l2(share(a.X, next, a.x_pitch, 0), a.pitch);
             if (rr) prefetch_l2(share(a.residual, next, a.r_pitch, 0), a.pitch);
@@ -387,7 +388,7 @@ cudaError_t norm_launch(const NormArgs &a, cudaStream_t s) {
     // thread: a lone row's time is its chain of latencies.
     const int64_t chunks = (int64_t)a.tiles_k * 32;
     int best = 10;
-    if (a.M <= 148) {
+    if (a.M <= kSms) {
         best = 5;
         while (best < 10 && ((int64_t)1 << best) < chunks) ++best;
     } else {
